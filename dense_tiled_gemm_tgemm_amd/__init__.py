@@ -52,9 +52,13 @@ from ._ops import (  # noqa: F401
     linear,
     linear_cross_entropy,
     tgemm_act_grad,
+    tgemm_act_grad_f32,
+    tgemm_act_grad_f32_workspace,
     tgemm_act_grad_workspace,
     tgemm_linear,
     tgemm_linear_grad,
+    tgemm_linear_grad_f32,
+    tgemm_linear_grad_f32_workspace,
     tgemm_linear_grad_workspace,
     tgemm_linear_workspace,
     tgemm_tn,

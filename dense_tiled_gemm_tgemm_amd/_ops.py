@@ -45,6 +45,8 @@ def _ops():
             "tgemm_tn_workspace": (_I64, [_I64, _I64, _I64, _INT, _I64, _I64, _INT, _I64, _INT, _INT, _INT]),
             "tgemm_act_grad": (_INT, [_I64, _I64, _INT, _P, _I64, _INT, _P, _I64, _P, _I64, _INT, _P, _P, _I64, _P]),
             "tgemm_act_grad_workspace": (_I64, [_I64, _I64]),
+            "tgemm_act_grad_f32": (_INT, [_I64, _I64, _INT, _P, _I64, _INT, _P, _I64, _P, _I64, _P, _INT, _P, _P, _I64, _P]),
+            "tgemm_act_grad_f32_workspace": (_I64, [_I64, _I64]),
             "tgemm_linear_grad": (_INT, [_I64, _I64, _I64, _INT, _P, _I64, _P, _I64, _INT, _INT, _P, _I64, _P, _I64, _P,
                                          _I64, _P, _I64, _INT, _P, _P, _I64, _P]),
             "tgemm_linear_grad_workspace": (_I64, [_I64, _I64, _I64, _INT, _I64, _I64, _INT, _INT, _I64, _I64, _I64]),
@@ -59,6 +61,8 @@ def _ops():
             "tgemm_xent_both_workspace": (_I64, [_I64, _I64, _I64, _INT, _I64, _I64, _I64, _I64]),
             "tgemm_scale": (_INT, [_INT, _I64, _P, _I64, _P, _P, _P]),
         }
+        for name in ("tgemm_linear_grad", "tgemm_linear_grad_workspace"):
+            sigs[name.replace("_grad", "_grad_f32")] = sigs[name]
         for name, (res, args) in sigs.items():
             fn = getattr(lib, name)
             fn.restype = res
@@ -109,6 +113,16 @@ def tgemm_act_grad_workspace(M, N) -> int:
     return int(_ops().tgemm_act_grad_workspace(M, N))
 
 
+def tgemm_act_grad_f32(M, N, type, dY, lddy, act, pre, ldpre, dP, lddp, scale, dbias_type="f32", dbias=None,
+                       workspace=None, workspace_bytes=0, stream=None) -> int:
+    return int(_ops().tgemm_act_grad_f32(M, N, _code(_DTYPE, type), dY, lddy, _code(_ACTS, act), pre, ldpre, dP, lddp, scale,
+                                         _code(_DTYPE, dbias_type), dbias, workspace, workspace_bytes, stream))
+
+
+def tgemm_act_grad_f32_workspace(M, N) -> int:
+    return int(_ops().tgemm_act_grad_f32_workspace(M, N))
+
+
 def tgemm_linear_grad(M, N, K, type, X, ldx, W, ldw, w_layout, act, pre, ldpre, dY, lddy, dX=None, lddx=0, dW=None,
                       lddw=0, dbias_type="f32", dbias=None, workspace=None, workspace_bytes=0, stream=None) -> int:
     return int(_ops().tgemm_linear_grad(M, N, K, _code(_DTYPE, type), X, ldx, W, ldw, _LAYOUT.get(w_layout, w_layout),
@@ -119,6 +133,19 @@ def tgemm_linear_grad(M, N, K, type, X, ldx, W, ldw, w_layout, act, pre, ldpre, 
 def tgemm_linear_grad_workspace(M, N, K, type, ldx, ldw, w_layout, act, lddy, lddx, lddw) -> int:
     return int(_ops().tgemm_linear_grad_workspace(M, N, K, _code(_DTYPE, type), ldx, ldw,
                                                   _LAYOUT.get(w_layout, w_layout), _code(_ACTS, act), lddy, lddx, lddw))
+
+
+def tgemm_linear_grad_f32(M, N, K, type, X, ldx, W, ldw, w_layout, act, pre, ldpre, dY, lddy, dX=None, lddx=0, dW=None,
+                          lddw=0, dbias_type="f32", dbias=None, workspace=None, workspace_bytes=0, stream=None) -> int:
+    return int(_ops().tgemm_linear_grad_f32(M, N, K, _code(_DTYPE, type), X, ldx, W, ldw, _LAYOUT.get(w_layout, w_layout),
+                                            _code(_ACTS, act), pre, ldpre, dY, lddy, dX, lddx, dW, lddw,
+                                            _code(_DTYPE, dbias_type), dbias, workspace, workspace_bytes, stream))
+
+
+def tgemm_linear_grad_f32_workspace(M, N, K, type, ldx, ldw, w_layout, act, lddy, lddx, lddw) -> int:
+    return int(_ops().tgemm_linear_grad_f32_workspace(M, N, K, _code(_DTYPE, type), ldx, ldw,
+                                                      _LAYOUT.get(w_layout, w_layout), _code(_ACTS, act), lddy, lddx,
+                                                      lddw))
 
 
 def tgemm_xent(rows, vocab, dim, type, H, ldh, W, ldw, target, ignore, reduction, lse, loss, total=None, count=None,
@@ -277,14 +304,14 @@ def _linear(torch, x, w, bias, act, residual, out_dtype, layout, keep_pre, tile_
 
 
 def _linear_grad(torch, x, w, act, pre, dy, layout, need_x, need_w, bias_dtype):
-    """(dx, dw, db) of 2-D operands as the forward call took them."""
+    """(dx, dw, db) of 2-D operands as the forward call took them; dy of the
+    operands' dtype or (an fp32 result's) float32."""
     M, K = x.shape
     N = dy.shape[1]
     dev = x.device
     dt = x.dtype
     code = TGEMM_BF16 if dt == torch.bfloat16 else TGEMM_F16
-    if dy.dtype != dt:
-        dy = dy.to(dt)
+    fn = "tgemm_linear_grad" if dy.dtype == dt else "tgemm_linear_grad_f32"
     x, ldx = _readable(x)
     w, ldw = _readable(w)
     dy, lddy = _readable(dy)
@@ -295,9 +322,9 @@ def _linear_grad(torch, x, w, act, pre, dy, layout, need_x, need_w, bias_dtype):
         dx = torch.empty((M, K), dtype=dt, device=dev) if need_x else None
         dw = torch.empty(w.shape, dtype=dt, device=dev) if need_w else None
         db = None if bias_dtype is None else torch.empty((N,), dtype=bias_dtype, device=dev)
-        need = _ws_size(dev.index, "tgemm_linear_grad_workspace", M, N, K, code, ldx, ldw, layout, act, lddy, ldk, lddw)
+        need = _ws_size(dev.index, fn + "_workspace", M, N, K, code, ldx, ldw, layout, act, lddy, ldk, lddw)
         ws, ws_ptr = _alloc(torch, need, dev)
-        rc = _ops().tgemm_linear_grad(
+        rc = getattr(_ops(), fn)(
             M, N, K, code, x.data_ptr(), ldx, w.data_ptr(), ldw, layout, act, None if pre is None else pre.data_ptr(), ldn,
             dy.data_ptr(), lddy, None if dx is None else dx.data_ptr(), ldk, None if dw is None else dw.data_ptr(), lddw,
             TGEMM_F32 if bias_dtype == torch.float32 else code, None if db is None else db.data_ptr(), ws_ptr, need,
@@ -477,8 +504,12 @@ def linear(x, weight, bias=None, act: str = "none", residual=None, out_dtype=Non
     row-major is copied first.
 
     Differentiable in x, weight, bias and residual. With an activation the
-    backward pass keeps the pre-activation in x's dtype. tile_m, splits, k_step:
-    explicit launch choices (tgemm_linear_config), without autograd.
+    backward pass keeps the pre-activation in x's dtype. The result's gradient,
+    times the activation's derivative, is rounded once to x's dtype for the
+    products (bias gradients sum it unrounded); where the result is float32 and x
+    float16 it is scaled by its largest value for that, so that gradients below
+    2^-25 and above 65504 keep their precision. tile_m, splits, k_step: explicit
+    launch choices (tgemm_linear_config), without autograd.
     """
     import torch
     if act not in _ACTS:

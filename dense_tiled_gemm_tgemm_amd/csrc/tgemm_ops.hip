@@ -591,11 +591,14 @@ extern "C" int64_t tgemm_linear_workspace(int64_t M, int64_t N, int64_t K, int t
     return tgemm_linear_config_workspace(M, N, K, type, ldx, ldw, w_layout, y_type, ldy, 0, 0, 0);
 }
 
-extern "C" int tgemm_linear_config(int64_t M, int64_t N, int64_t K, int type, const void* X, int64_t ldx, const void* W,
-                                   int64_t ldw, int w_layout, const void* bias, int bias_type, int act,
-                                   const void* residual, int64_t ldr, int y_type, void* Y, int64_t ldy, void* pre,
-                                   int64_t ldpre, float alpha, void* workspace, int64_t workspace_bytes, void* stream,
-                                   int tile_m, int k_step, int splits) {
+namespace tg {
+namespace {
+
+// tgemm_linear_config; alpha_dev: null, or one device value alpha is multiplied by.
+int linear_call(int64_t M, int64_t N, int64_t K, int type, const void* X, int64_t ldx, const void* W, int64_t ldw,
+                int w_layout, const void* bias, int bias_type, int act, const void* residual, int64_t ldr, int y_type,
+                void* Y, int64_t ldy, void* pre, int64_t ldpre, float alpha, const float* alpha_dev, void* workspace,
+                int64_t workspace_bytes, void* stream, int tile_m, int k_step, int splits) {
     if (act < TGEMM_ACT_NONE || act > TGEMM_ACT_GELU_TANH) return TGEMM_ERR_INVALID;
     if (check_dims(M, N, K) != TGEMM_OK || !is16(type) || (y_type != type && y_type != TGEMM_F32)) return TGEMM_ERR_INVALID;
     if (w_layout != TGEMM_B_KxN && w_layout != TGEMM_B_NxK) return TGEMM_ERR_INVALID;
@@ -631,6 +634,7 @@ extern "C" int tgemm_linear_config(int64_t M, int64_t N, int64_t K, int type, co
     a.N = (int)N;
     a.K = (int)K;
     a.alpha = alpha;
+    a.alpha_dev = alpha_dev;
     a.biasv = bias;
     a.bias_f32 = bias_type == TGEMM_F32;
     a.act = act;
@@ -639,6 +643,18 @@ extern "C" int tgemm_linear_config(int64_t M, int64_t N, int64_t K, int type, co
     a.res = residual;
     a.ldres = residual ? ldr : 0;
     return run_linear(a, type == TGEMM_BF16, nxk, y_type == TGEMM_F32, type, pl, ncu, workspace, stream);
+}
+
+}  // namespace
+}  // namespace tg
+
+extern "C" int tgemm_linear_config(int64_t M, int64_t N, int64_t K, int type, const void* X, int64_t ldx, const void* W,
+                                   int64_t ldw, int w_layout, const void* bias, int bias_type, int act,
+                                   const void* residual, int64_t ldr, int y_type, void* Y, int64_t ldy, void* pre,
+                                   int64_t ldpre, float alpha, void* workspace, int64_t workspace_bytes, void* stream,
+                                   int tile_m, int k_step, int splits) {
+    return linear_call(M, N, K, type, X, ldx, W, ldw, w_layout, bias, bias_type, act, residual, ldr, y_type, Y, ldy, pre,
+                       ldpre, alpha, nullptr, workspace, workspace_bytes, stream, tile_m, k_step, splits);
 }
 
 extern "C" int tgemm_linear(int64_t M, int64_t N, int64_t K, int type, const void* X, int64_t ldx, const void* W,
@@ -657,9 +673,13 @@ extern "C" int64_t tgemm_tn_workspace(int64_t M, int64_t N, int64_t K, int type,
     return rc != TGEMM_OK ? rc : pl.ws;
 }
 
-extern "C" int tgemm_tn(int64_t M, int64_t N, int64_t K, int type, const void* A, int64_t lda, const void* B, int64_t ldb,
-                        int c_type, void* C, int64_t ldc, float alpha, int accumulate, void* workspace,
-                        int64_t workspace_bytes, void* stream, int tile_m, int k_step, int splits) {
+namespace tg {
+namespace {
+
+// tgemm_tn; alpha_dev as in linear_call.
+int tn_call(int64_t M, int64_t N, int64_t K, int type, const void* A, int64_t lda, const void* B, int64_t ldb, int c_type,
+            void* C, int64_t ldc, float alpha, const float* alpha_dev, int accumulate, void* workspace,
+            int64_t workspace_bytes, void* stream, int tile_m, int k_step, int splits) {
     if (accumulate != 0 && accumulate != 1) return TGEMM_ERR_INVALID;
     if (check_dims(M, N, K) != TGEMM_OK || !is16(type) || (c_type != type && c_type != TGEMM_F32)) return TGEMM_ERR_INVALID;
     Mem ma, mb, mc;
@@ -684,9 +704,20 @@ extern "C" int tgemm_tn(int64_t M, int64_t N, int64_t K, int type, const void* A
     a.N = (int)N;
     a.K = (int)K;
     a.alpha = alpha;
+    a.alpha_dev = alpha_dev;
     a.res = accumulate ? C : nullptr;
     a.ldres = accumulate ? ldc : 0;
     return run_tn(a, type == TGEMM_BF16, c_type == TGEMM_F32, pl, ncu, workspace, stream);
+}
+
+}  // namespace
+}  // namespace tg
+
+extern "C" int tgemm_tn(int64_t M, int64_t N, int64_t K, int type, const void* A, int64_t lda, const void* B, int64_t ldb,
+                        int c_type, void* C, int64_t ldc, float alpha, int accumulate, void* workspace,
+                        int64_t workspace_bytes, void* stream, int tile_m, int k_step, int splits) {
+    return tn_call(M, N, K, type, A, lda, B, ldb, c_type, C, ldc, alpha, nullptr, accumulate, workspace, workspace_bytes,
+                   stream, tile_m, k_step, splits);
 }
 
 extern "C" int64_t tgemm_act_grad_workspace(int64_t M, int64_t N) {
@@ -694,69 +725,126 @@ extern "C" int64_t tgemm_act_grad_workspace(int64_t M, int64_t N) {
     return ceil_div(M, col_rows(M, N)) * N * 4;
 }
 
-extern "C" int tgemm_act_grad(int64_t M, int64_t N, int type, const void* dY, int64_t lddy, int act, const void* pre,
-                              int64_t ldpre, void* dP, int64_t lddp, int dbias_type, void* dbias, void* workspace,
-                              int64_t workspace_bytes, void* stream) {
+namespace tg {
+namespace {
+
+// Workgroups of tgemm_largest_kernel: 256 columns and 64 rows each at least, 1024
+// at most (every workgroup of the kernel after it reads all their maxima).
+void largest_grid(int64_t M, int64_t N, int64_t* gx, int64_t* gy) {
+    *gx = ceil_div(N, 256) < 256 ? ceil_div(N, 256) : 256;
+    const int64_t most = 1024 / *gx;
+    *gy = ceil_div(M, 64) < most ? ceil_div(M, 64) : most;
+}
+
+template <int AB, bool G32>
+const void* act_grad_kernel(int act) {
+    static const void* const fns[5] = {
+        (const void*)&tgemm_act_grad_kernel<AB, kActNone, G32>, (const void*)&tgemm_act_grad_kernel<AB, kActRelu, G32>,
+        (const void*)&tgemm_act_grad_kernel<AB, kActSilu, G32>, (const void*)&tgemm_act_grad_kernel<AB, kActGelu, G32>,
+        (const void*)&tgemm_act_grad_kernel<AB, kActGeluTanh, G32>};
+    return fns[act];
+}
+
+// Workspace: the column blocks' sums, behind them (fp32 dY) the parts' maxima.
+int64_t act_grad_parts(int64_t M, int64_t N) { return ceil_div(M, col_rows(M, N)) * N * 4; }
+constexpr int64_t kTopsBytes = 1024 * 4;
+
+// tgemm_act_grad, tgemm_act_grad_f32 (f32).
+int act_grad_call(int64_t M, int64_t N, int type, bool f32, const void* dY, int64_t lddy, int act, const void* pre,
+                  int64_t ldpre, void* dP, int64_t lddp, float* scale, int dbias_type, void* dbias, void* workspace,
+                  int64_t workspace_bytes, void* stream) {
     if (check_dims(M, N, 0) != TGEMM_OK || !is16(type)) return TGEMM_ERR_INVALID;
     if (act < TGEMM_ACT_NONE || act > TGEMM_ACT_GELU_TANH) return TGEMM_ERR_INVALID;
     if (dbias && dbias_type != type && dbias_type != TGEMM_F32) return TGEMM_ERR_INVALID;
-    Mem my, mp{}, md{}, mb{};
-    if (!array_ok(dY, M, N, lddy, 2, &my)) return TGEMM_ERR_INVALID;
-    if (act == TGEMM_ACT_NONE) {
-        if (pre || dP) return TGEMM_ERR_INVALID;
-    } else if (!array_ok(pre, M, N, ldpre, 2, &mp) || !array_ok(dP, M, N, lddp, 2, &md)) {
-        return TGEMM_ERR_INVALID;
-    }
-    if (dbias && !array_ok(dbias, 1, N, N > 1 ? N : 1, esize(dbias_type), &mb)) return TGEMM_ERR_INVALID;
-    if (meet(md, my) || meet(md, mp) || meet(mb, my) || meet(mb, mp) || meet(mb, md)) return TGEMM_ERR_INVALID;
+    Mem in[2] = {}, out[3] = {};
+    if (!array_ok(dY, M, N, lddy, f32 ? 4 : 2, &in[0])) return TGEMM_ERR_INVALID;
+    if (act == TGEMM_ACT_NONE ? pre != nullptr : !array_ok(pre, M, N, ldpre, 2, &in[1])) return TGEMM_ERR_INVALID;
+    const bool may = f32 ? !dP : act == TGEMM_ACT_NONE;       // calls without dP
+    if (may ? dP != nullptr : !array_ok(dP, M, N, lddp, 2, &out[0])) return TGEMM_ERR_INVALID;
+    if (dbias && !array_ok(dbias, 1, N, N > 1 ? N : 1, esize(dbias_type), &out[1])) return TGEMM_ERR_INVALID;
+    if (f32 && ((scale != nullptr) != (dP != nullptr) || (scale && !array_ok(scale, 1, 1, 1, 4, &out[2])))) return TGEMM_ERR_INVALID;
+    if (outputs_meet(in, 2, out, 3)) return TGEMM_ERR_INVALID;
     int per = col_rows(M, N);
     const int64_t blocks = ceil_div(M, per);
-    const int64_t need = dbias ? blocks * N * 4 : 0;
+    const int64_t parts = dbias ? blocks * N * 4 : 0;
+    const bool largest = f32 && dP && type == TGEMM_F16 && M > 0 && N > 0;
+    const int64_t need = parts + (largest ? kTopsBytes : 0);
     if (!ws_ok(workspace, workspace_bytes, need)) return TGEMM_ERR_INVALID;
     const Mem mws{workspace, (uint64_t)need};
-    if (meet(mws, my) || meet(mws, mp) || meet(mws, md) || meet(mws, mb)) return TGEMM_ERR_INVALID;
-    if (N == 0 || (act == TGEMM_ACT_NONE && !dbias)) return TGEMM_OK;
+    if (outputs_meet(in, 2, &mws, 1) || outputs_meet(out, 3, &mws, 1)) return TGEMM_ERR_INVALID;
+    if (N == 0 || (!dP && !dbias)) return TGEMM_OK;
     const int ab = type == TGEMM_BF16;
     float* part = dbias ? static_cast<float*>(workspace) : nullptr;
     int m = (int)M, n = (int)N;
     if (M > 0) {
-        void* kargs[] = {&dY, &lddy, &pre, &ldpre, &dP, &lddp, &part, &m, &n, &per};
-        const void* fns[2][5] = {
-            {(const void*)&tgemm_act_grad_kernel<0, kActNone>, (const void*)&tgemm_act_grad_kernel<0, kActRelu>,
-             (const void*)&tgemm_act_grad_kernel<0, kActSilu>, (const void*)&tgemm_act_grad_kernel<0, kActGelu>,
-             (const void*)&tgemm_act_grad_kernel<0, kActGeluTanh>},
-            {(const void*)&tgemm_act_grad_kernel<1, kActNone>, (const void*)&tgemm_act_grad_kernel<1, kActRelu>,
-             (const void*)&tgemm_act_grad_kernel<1, kActSilu>, (const void*)&tgemm_act_grad_kernel<1, kActGelu>,
-             (const void*)&tgemm_act_grad_kernel<1, kActGeluTanh>}};
-        const int rc = launch_k(fns[ab][act], ceil_div(N, 256), blocks, 256, kargs, stream);
+        const float* tops = nullptr;
+        int ntops = 0;
+        if (largest) {
+            int64_t gx, gy;
+            largest_grid(M, N, &gx, &gy);
+            ntops = (int)(gx * gy);
+            float* t = reinterpret_cast<float*>(static_cast<char*>(workspace) + parts);
+            tops = t;
+            void* kargs[] = {&dY, &lddy, &m, &n, &t};
+            const int rc = launch_k((const void*)&tgemm_largest_kernel, gx, gy, 256, kargs, stream);
+            if (rc != TGEMM_OK) return rc;
+        }
+        void* kargs[] = {&dY, &lddy, &pre, &ldpre, &dP, &lddp, &part, &m, &n, &per, &tops, &ntops, &scale};
+        const void* fn = f32 ? (ab ? act_grad_kernel<1, true>(act) : act_grad_kernel<0, true>(act))
+                             : (ab ? act_grad_kernel<1, false>(act) : act_grad_kernel<0, false>(act));
+        const int rc = launch_k(fn, ceil_div(N, 256), blocks, 256, kargs, stream);
         if (rc != TGEMM_OK) return rc;
     }
     if (!dbias) return TGEMM_OK;
-    int nb = (int)blocks, f32 = dbias_type == TGEMM_F32;
+    int nb = (int)blocks, out32 = dbias_type == TGEMM_F32;
     const float* cpart = part;
-    void* kargs[] = {&cpart, &nb, &n, &dbias, &f32};
+    void* kargs[] = {&cpart, &nb, &n, &dbias, &out32};
     return launch_k(ab ? (const void*)&tgemm_colsum_join_kernel<1> : (const void*)&tgemm_colsum_join_kernel<0>,
                     ceil_div(N, 64), 1, 256, kargs, stream);
+}
+
+}  // namespace
+}  // namespace tg
+
+extern "C" int tgemm_act_grad(int64_t M, int64_t N, int type, const void* dY, int64_t lddy, int act, const void* pre,
+                              int64_t ldpre, void* dP, int64_t lddp, int dbias_type, void* dbias, void* workspace,
+                              int64_t workspace_bytes, void* stream) {
+    return act_grad_call(M, N, type, false, dY, lddy, act, pre, ldpre, dP, lddp, nullptr, dbias_type, dbias, workspace,
+                         workspace_bytes, stream);
+}
+
+extern "C" int64_t tgemm_act_grad_f32_workspace(int64_t M, int64_t N) {
+    if (check_dims(M, N, 0) != TGEMM_OK) return TGEMM_ERR_INVALID;
+    return act_grad_parts(M, N) + kTopsBytes;
+}
+
+extern "C" int tgemm_act_grad_f32(int64_t M, int64_t N, int type, const float* dY, int64_t lddy, int act, const void* pre,
+                                  int64_t ldpre, void* dP, int64_t lddp, float* scale, int dbias_type, void* dbias,
+                                  void* workspace, int64_t workspace_bytes, void* stream) {
+    return act_grad_call(M, N, type, true, dY, lddy, act, pre, ldpre, dP, lddp, scale, dbias_type, dbias, workspace,
+                         workspace_bytes, stream);
 }
 
 namespace tg {
 namespace {
 
-// Gradients of a linear layer: dP (with an activation) in rows of a multiple of
-// 64 elements, then one area that the three steps use in turn.
+// Gradients of a linear layer: dP (with an activation, or from an fp32 dY, whose
+// factor lies behind it) in rows of a multiple of 64 elements, then one area that
+// the three steps use in turn.
 struct LinGradPlan {
-    int64_t ldp, off, ws;
+    int64_t ldp, off_scale, off, ws;
 };
 
-int plan_linear_grad(int64_t M, int64_t N, int64_t K, int type, int64_t ldx, int64_t ldw, int w_layout, int act,
+int plan_linear_grad(int64_t M, int64_t N, int64_t K, int type, bool f32, int64_t ldx, int64_t ldw, int w_layout, int act,
                      int64_t lddy, int64_t lddx, int64_t lddw, LinGradPlan* x) {
     if (check_dims(M, N, K) != TGEMM_OK || !is16(type)) return TGEMM_ERR_INVALID;
     if (w_layout != TGEMM_B_KxN && w_layout != TGEMM_B_NxK) return TGEMM_ERR_INVALID;
     if (act < TGEMM_ACT_NONE || act > TGEMM_ACT_GELU_TANH) return TGEMM_ERR_INVALID;
     if (lddy < (N > 1 ? N : 1)) return TGEMM_ERR_INVALID;
-    const bool nxk = w_layout == TGEMM_B_NxK;
-    x->ldp = act == TGEMM_ACT_NONE ? lddy : up(N > 0 ? N : 1, 64);
-    x->off = act == TGEMM_ACT_NONE ? 0 : up(M * x->ldp * 2, 256);
+    const bool nxk = w_layout == TGEMM_B_NxK, own = f32 || act != TGEMM_ACT_NONE;
+    x->ldp = own ? up(N > 0 ? N : 1, 64) : lddy;
+    x->off_scale = own ? up(M * x->ldp * 2, 256) : 0;
+    x->off = x->off_scale + (f32 ? 256 : 0);
     OpPlan dx, dw;
     int ncu;
     int rc = plan_linear(M, K, N, type, x->ldp, ldw, nxk ? TGEMM_B_KxN : TGEMM_B_NxK, type, lddx, 0, 0, 0, &ncu, &dx);
@@ -764,27 +852,18 @@ int plan_linear_grad(int64_t M, int64_t N, int64_t K, int type, int64_t ldx, int
     rc = nxk ? plan_tn(N, K, M, type, x->ldp, ldx, type, lddw, 0, 0, 0, &ncu, &dw)
              : plan_tn(K, N, M, type, ldx, x->ldp, type, lddw, 0, 0, 0, &ncu, &dw);
     if (rc != TGEMM_OK) return rc;
-    int64_t most = tgemm_act_grad_workspace(M, N);
+    int64_t most = act_grad_parts(M, N) + (f32 ? kTopsBytes : 0);
     most = most > dx.ws ? most : dx.ws;
     most = most > dw.ws ? most : dw.ws;
     x->ws = x->off + most;
     return TGEMM_OK;
 }
 
-}  // namespace
-}  // namespace tg
-
-extern "C" int64_t tgemm_linear_grad_workspace(int64_t M, int64_t N, int64_t K, int type, int64_t ldx, int64_t ldw,
-                                               int w_layout, int act, int64_t lddy, int64_t lddx, int64_t lddw) {
-    LinGradPlan x;
-    const int rc = plan_linear_grad(M, N, K, type, ldx, ldw, w_layout, act, lddy, lddx, lddw, &x);
-    return rc != TGEMM_OK ? rc : x.ws;
-}
-
-extern "C" int tgemm_linear_grad(int64_t M, int64_t N, int64_t K, int type, const void* X, int64_t ldx, const void* W,
-                                 int64_t ldw, int w_layout, int act, const void* pre, int64_t ldpre, const void* dY,
-                                 int64_t lddy, void* dX, int64_t lddx, void* dW, int64_t lddw, int dbias_type, void* dbias,
-                                 void* workspace, int64_t workspace_bytes, void* stream) {
+// tgemm_linear_grad, tgemm_linear_grad_f32 (f32).
+int linear_grad_call(int64_t M, int64_t N, int64_t K, int type, bool f32, const void* X, int64_t ldx, const void* W,
+                     int64_t ldw, int w_layout, int act, const void* pre, int64_t ldpre, const void* dY, int64_t lddy,
+                     void* dX, int64_t lddx, void* dW, int64_t lddw, int dbias_type, void* dbias, void* workspace,
+                     int64_t workspace_bytes, void* stream) {
     if (check_dims(M, N, K) != TGEMM_OK || !is16(type)) return TGEMM_ERR_INVALID;
     if (w_layout != TGEMM_B_KxN && w_layout != TGEMM_B_NxK) return TGEMM_ERR_INVALID;
     if (act < TGEMM_ACT_NONE || act > TGEMM_ACT_GELU_TANH) return TGEMM_ERR_INVALID;
@@ -792,7 +871,8 @@ extern "C" int tgemm_linear_grad(int64_t M, int64_t N, int64_t K, int type, cons
     const bool nxk = w_layout == TGEMM_B_NxK;
     const int64_t wr = nxk ? N : K, wc = nxk ? K : N;
     Mem in[4] = {}, out[3] = {};
-    if (!array_ok(X, M, K, ldx, 2, &in[0]) || !array_ok(W, wr, wc, ldw, 2, &in[1]) || !array_ok(dY, M, N, lddy, 2, &in[2]))
+    if (!array_ok(X, M, K, ldx, 2, &in[0]) || !array_ok(W, wr, wc, ldw, 2, &in[1]) ||
+        !array_ok(dY, M, N, lddy, f32 ? 4 : 2, &in[2]))
         return TGEMM_ERR_INVALID;
     if (act == TGEMM_ACT_NONE ? pre != nullptr : !array_ok(pre, M, N, ldpre, 2, &in[3])) return TGEMM_ERR_INVALID;
     if (dX && !array_ok(dX, M, K, lddx, 2, &out[0])) return TGEMM_ERR_INVALID;
@@ -800,7 +880,7 @@ extern "C" int tgemm_linear_grad(int64_t M, int64_t N, int64_t K, int type, cons
     if (dbias && !array_ok(dbias, 1, N, N > 1 ? N : 1, esize(dbias_type), &out[2])) return TGEMM_ERR_INVALID;
     if (outputs_meet(in, 4, out, 3)) return TGEMM_ERR_INVALID;
     LinGradPlan x;
-    int rc = plan_linear_grad(M, N, K, type, ldx, ldw, w_layout, act, lddy, dX ? lddx : (K > 1 ? K : 1),
+    int rc = plan_linear_grad(M, N, K, type, f32, ldx, ldw, w_layout, act, lddy, dX ? lddx : (K > 1 ? K : 1),
                               dW ? lddw : (wc > 1 ? wc : 1), &x);
     if (rc != TGEMM_OK) return rc;
     if (!ws_ok(workspace, workspace_bytes, x.ws)) return TGEMM_ERR_INVALID;
@@ -809,25 +889,63 @@ extern "C" int tgemm_linear_grad(int64_t M, int64_t N, int64_t K, int type, cons
     const bool products = (dX && M > 0 && K > 0) || (dW && N > 0 && K > 0);
     const void* dP = dY;
     int64_t ldp = lddy;
+    float* scale = f32 ? reinterpret_cast<float*>(static_cast<char*>(workspace) + x.off_scale) : nullptr;
     char* area = static_cast<char*>(workspace) + x.off;
     const int64_t left = x.ws - x.off;
-    if (act != TGEMM_ACT_NONE && (products || dbias)) {
-        rc = tgemm_act_grad(M, N, type, dY, lddy, act, pre, ldpre, workspace, x.ldp, dbias_type, dbias, area, left, stream);
+    if ((f32 || act != TGEMM_ACT_NONE) && (products || (dbias && !f32))) {
+        rc = act_grad_call(M, N, type, f32, dY, lddy, act, pre, ldpre, workspace, x.ldp, scale, dbias_type, dbias, area, left,
+                           stream);
         dP = workspace;
         ldp = x.ldp;
     } else if (dbias) {
-        rc = tgemm_act_grad(M, N, type, dY, lddy, act, nullptr, 0, nullptr, 0, dbias_type, dbias, area, left, stream);
+        rc = act_grad_call(M, N, type, f32, dY, lddy, act, f32 ? pre : nullptr, ldpre, nullptr, 0, nullptr, dbias_type, dbias,
+                           area, left, stream);
     }
     if (rc != TGEMM_OK) return rc;
+    // (the factor of binary16's dP; of an empty dP none has been written)
+    const float* undo = f32 && type == TGEMM_F16 && M > 0 && N > 0 ? scale : nullptr;
     if (dX) {
-        rc = tgemm_linear(M, K, N, type, dP, ldp, W, ldw, nxk ? TGEMM_B_KxN : TGEMM_B_NxK, nullptr, TGEMM_F32, TGEMM_ACT_NONE,
-                          nullptr, 0, type, dX, lddx, nullptr, 0, 1.0f, area, left, stream);
+        rc = linear_call(M, K, N, type, dP, ldp, W, ldw, nxk ? TGEMM_B_KxN : TGEMM_B_NxK, nullptr, TGEMM_F32, TGEMM_ACT_NONE,
+                         nullptr, 0, type, dX, lddx, nullptr, 0, 1.0f, undo, area, left, stream, 0, 0, 0);
         if (rc != TGEMM_OK) return rc;
     }
     if (dW)
-        rc = nxk ? tgemm_tn(N, K, M, type, dP, ldp, X, ldx, type, dW, lddw, 1.0f, 0, area, left, stream, 0, 0, 0)
-                 : tgemm_tn(K, N, M, type, X, ldx, dP, ldp, type, dW, lddw, 1.0f, 0, area, left, stream, 0, 0, 0);
+        rc = nxk ? tn_call(N, K, M, type, dP, ldp, X, ldx, type, dW, lddw, 1.0f, undo, 0, area, left, stream, 0, 0, 0)
+                 : tn_call(K, N, M, type, X, ldx, dP, ldp, type, dW, lddw, 1.0f, undo, 0, area, left, stream, 0, 0, 0);
     return rc;
+}
+
+}  // namespace
+}  // namespace tg
+
+extern "C" int64_t tgemm_linear_grad_workspace(int64_t M, int64_t N, int64_t K, int type, int64_t ldx, int64_t ldw,
+                                               int w_layout, int act, int64_t lddy, int64_t lddx, int64_t lddw) {
+    LinGradPlan x;
+    const int rc = plan_linear_grad(M, N, K, type, false, ldx, ldw, w_layout, act, lddy, lddx, lddw, &x);
+    return rc != TGEMM_OK ? rc : x.ws;
+}
+
+extern "C" int tgemm_linear_grad(int64_t M, int64_t N, int64_t K, int type, const void* X, int64_t ldx, const void* W,
+                                 int64_t ldw, int w_layout, int act, const void* pre, int64_t ldpre, const void* dY,
+                                 int64_t lddy, void* dX, int64_t lddx, void* dW, int64_t lddw, int dbias_type, void* dbias,
+                                 void* workspace, int64_t workspace_bytes, void* stream) {
+    return linear_grad_call(M, N, K, type, false, X, ldx, W, ldw, w_layout, act, pre, ldpre, dY, lddy, dX, lddx, dW, lddw,
+                            dbias_type, dbias, workspace, workspace_bytes, stream);
+}
+
+extern "C" int64_t tgemm_linear_grad_f32_workspace(int64_t M, int64_t N, int64_t K, int type, int64_t ldx, int64_t ldw,
+                                                   int w_layout, int act, int64_t lddy, int64_t lddx, int64_t lddw) {
+    LinGradPlan x;
+    const int rc = plan_linear_grad(M, N, K, type, true, ldx, ldw, w_layout, act, lddy, lddx, lddw, &x);
+    return rc != TGEMM_OK ? rc : x.ws;
+}
+
+extern "C" int tgemm_linear_grad_f32(int64_t M, int64_t N, int64_t K, int type, const void* X, int64_t ldx, const void* W,
+                                     int64_t ldw, int w_layout, int act, const void* pre, int64_t ldpre, const float* dY,
+                                     int64_t lddy, void* dX, int64_t lddx, void* dW, int64_t lddw, int dbias_type,
+                                     void* dbias, void* workspace, int64_t workspace_bytes, void* stream) {
+    return linear_grad_call(M, N, K, type, true, X, ldx, W, ldw, w_layout, act, pre, ldpre, dY, lddy, dX, lddx, dW, lddw,
+                            dbias_type, dbias, workspace, workspace_bytes, stream);
 }
 
 extern "C" int64_t tgemm_xent_workspace(int64_t rows, int64_t vocab, int64_t dim, int type, int64_t ldh, int64_t ldw) {

@@ -382,12 +382,46 @@ __global__ void __launch_bounds__(256) tgemm_tn_narrow_kernel(OpArgs a, float* s
 // per block of `rows` rows. A workgroup owns 256 columns x `rows` rows: 32
 // lanes x 8 columns (16 bytes), 8 rows side by side, so every wave instruction
 // reads two whole 512-byte row pieces. Bound by HBM: three arrays of M x N once.
+//
+// G32: dy is fp32, dp (where it is not null, with any ACT) is rounded once, and
+// the column sums are of values that were never rounded. Binary16 holds neither
+// the 1e-8 of a mean over a large result nor a gradient past 65504, so dp is
+// multiplied there by the power of two that takes the largest |dy| into
+// [2^14, 2^15) (no derivative here exceeds 1.13; exact, but for what falls 2^39
+// below the largest); `tops` holds ntops maxima of parts of |dy|, `scale`
+// receives what undoes the factor after the products. bfloat16 has fp32's range:
+// tops is null, the factor 1. dy goes through HBM twice with binary16 (8192 x 8192,
+// silu: 150 us, 108 with bfloat16; a cast of dy before the kernel of 16-bit values,
+// 155).
+__device__ __forceinline__ float largest_exponent_factor(float m, int* shift) {
+    int s = m > 0.f ? 15 - __builtin_amdgcn_frexp_expf(m) : 0;
+    s = s > 126 ? 126 : s;                            // 2^-s stays normal (s >= 15 - 128)
+    *shift = s;
+    return ldexpf(1.0f, s);
+}
 
-template <int AB, int ACT>
+template <int AB, int ACT, bool G32 = false>
 __global__ void __launch_bounds__(256)
-tgemm_act_grad_kernel(const uint16_t* dy, int64_t lddy, const uint16_t* pre, int64_t ldpre, uint16_t* dp, int64_t lddp,
-                      float* part, int M, int N, int rows) {
+tgemm_act_grad_kernel(const void* dyv, int64_t lddy, const uint16_t* pre, int64_t ldpre, uint16_t* dp, int64_t lddp,
+                      float* part, int M, int N, int rows, const float* tops, int ntops, float* scale) {
+    using Dy = std::conditional_t<G32, float, uint16_t>;
+    constexpr bool kDp = G32 || ACT != kActNone;
     __shared__ float red[8][32][9];
+    const Dy* dy = static_cast<const Dy*>(dyv);
+    float up = 1.0f;
+    if constexpr (G32) {
+        int shift = 0;
+        if (tops) {
+            __shared__ float rm[4];
+            float m = 0.f;
+            for (int i = threadIdx.x; i < ntops; i += 256) m = fmaxf(m, tops[i]);
+            for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+            if ((threadIdx.x & 63) == 0) rm[threadIdx.x >> 6] = m;
+            __syncthreads();
+            up = largest_exponent_factor(fmaxf(fmaxf(rm[0], rm[1]), fmaxf(rm[2], rm[3])), &shift);
+        }
+        if (scale && (blockIdx.x | blockIdx.y | threadIdx.x) == 0) *scale = ldexpf(1.0f, -shift);
+    }
     const int c = threadIdx.x & 31, r = threadIdx.x >> 5;
     const int col = (int)blockIdx.x * 256 + 8 * c;
     const int row0 = (int)blockIdx.y * rows;
@@ -399,9 +433,30 @@ tgemm_act_grad_kernel(const uint16_t* dy, int64_t lddy, const uint16_t* pre, int
         for (int q = 0; q < rows / 8; ++q) {
             const int row = row0 + 8 * q + r;
             if (row >= M) break;
-            const uint16_t* gy = dy + (int64_t)row * lddy + col;
-            u32x4 v, w{};
-            v = n == 8 ? *reinterpret_cast<const u32x4u*>(gy) : load8_elems(gy, n);
+            const Dy* gy = dy + (int64_t)row * lddy + col;
+            float gv[8];
+            u32x4 w{};
+            if constexpr (G32) {
+                typedef f32x4 __attribute__((aligned(4))) f32x4u;
+                if (n == 8) {
+                    const f32x4 a = *reinterpret_cast<const f32x4u*>(gy), b = *reinterpret_cast<const f32x4u*>(gy + 4);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        gv[e] = a[e];
+                        gv[4 + e] = b[e];
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) gv[e] = e < n ? gy[e] : 0.f;
+                }
+            } else {
+                const u32x4 v = n == 8 ? *reinterpret_cast<const u32x4u*>(gy) : load8_elems(gy, n);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    gv[2 * e] = lo16<AB>(v[e]);
+                    gv[2 * e + 1] = hi16<AB>(v[e]);
+                }
+            }
             if constexpr (ACT != kActNone) {
                 const uint16_t* gp = pre + (int64_t)row * ldpre + col;
                 w = n == 8 ? *reinterpret_cast<const u32x4u*>(gp) : load8_elems(gp, n);
@@ -409,16 +464,16 @@ tgemm_act_grad_kernel(const uint16_t* dy, int64_t lddy, const uint16_t* pre, int
             u32x4 o{};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                float lo = lo16<AB>(v[e]), hi = hi16<AB>(v[e]);
+                float lo = gv[2 * e], hi = gv[2 * e + 1];
                 if constexpr (ACT != kActNone) {
                     lo *= act_grad<ACT>(lo16<AB>(w[e]));
                     hi *= act_grad<ACT>(hi16<AB>(w[e]));
-                    o[e] = pack2<AB>(lo, hi);
                 }
+                if constexpr (kDp) o[e] = G32 ? pack2<AB>(lo * up, hi * up) : pack2<AB>(lo, hi);
                 s[2 * e] += lo;
                 s[2 * e + 1] += hi;
             }
-            if constexpr (ACT != kActNone) {
+            if (kDp && (!G32 || dp)) {
                 uint16_t* go = dp + (int64_t)row * lddp + col;
                 if (n == 8) {
                     *reinterpret_cast<u32x4u*>(go) = o;
@@ -440,6 +495,39 @@ tgemm_act_grad_kernel(const uint16_t* dy, int64_t lddy, const uint16_t* pre, int
     for (int q = 0; q < 8; ++q) t += red[q][cc][e];
     const int ccol = (int)blockIdx.x * 256 + 8 * cc + e;
     if (ccol < N) part[(int64_t)blockIdx.y * N + ccol] = t;
+}
+
+// The largest finite |dy| of the parts of an fp32 M x N array (G32 above): a
+// workgroup takes every gridDim.x-th 256 columns of every gridDim.y-th 8 rows.
+// Infinities and NaN do not count: the factor stays that of the other values.
+__global__ void __launch_bounds__(256)
+tgemm_largest_kernel(const float* dy, int64_t lddy, int M, int N, float* tops) {
+    __shared__ float rm[4];
+    const int c = threadIdx.x & 31, r = threadIdx.x >> 5;
+    float m = 0.f;
+    auto take = [&](float v) {
+        v = __builtin_fabsf(v);
+        m = fmaxf(m, v < __builtin_inff() ? v : 0.f);
+    };
+    for (int64_t row = (int64_t)blockIdx.y * 8 + r; row < M; row += (int64_t)gridDim.y * 8)
+        for (int64_t col = (int64_t)blockIdx.x * 256 + 8 * c; col < N; col += (int64_t)gridDim.x * 256) {
+            typedef f32x4 __attribute__((aligned(4))) f32x4u;
+            const float* p = dy + row * lddy + col;
+            if (col + 8 <= N) {
+                const f32x4 a = *reinterpret_cast<const f32x4u*>(p), b = *reinterpret_cast<const f32x4u*>(p + 4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    take(a[e]);
+                    take(b[e]);
+                }
+            } else {
+                for (int e = 0; col + e < N; ++e) take(p[e]);
+            }
+        }
+    for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+    if ((threadIdx.x & 63) == 0) rm[threadIdx.x >> 6] = m;
+    __syncthreads();
+    if (threadIdx.x == 0) tops[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = fmaxf(fmaxf(rm[0], rm[1]), fmaxf(rm[2], rm[3]));
 }
 
 // Column sums of the row blocks' parts, in row order: four waves take a

@@ -125,6 +125,29 @@ int tgemm_linear_grad(int64_t M, int64_t N, int64_t K, int type, const void* X, 
                       int64_t lddx, void* dW, int64_t lddw, int dbias_type, void* dbias, void* workspace,
                       int64_t workspace_bytes, void* stream);
 
+/*
+ * tgemm_act_grad and tgemm_linear_grad for a dY in fp32 (an fp32 Y's gradient),
+ * which is rounded once, as dP, after the product with act'(pre); dbias sums
+ * values that were not rounded. Binary16 would lose values below 2^-25 and above
+ * 65504: dP is multiplied there by the power of two 1 / *scale that takes the
+ * largest finite |dY| into [2^14, 2^15) (bfloat16: *scale is 1).
+ *   tgemm_act_grad_f32: dP = dY * act'(pre) / *scale, or NULL where only dbias is
+ *     wanted; scale: one fp32 in device memory, NULL where dP is; it is not
+ *     written where M or N is 0. TGEMM_ACT_NONE: pre must be NULL, dP is dY / *scale.
+ *   tgemm_linear_grad_f32: the factor is undone in fp32 at the end of both
+ *     products, before the one rounding of dX and dW.
+ */
+int64_t tgemm_act_grad_f32_workspace(int64_t M, int64_t N);
+int tgemm_act_grad_f32(int64_t M, int64_t N, int type, const float* dY, int64_t lddy, int act, const void* pre,
+                       int64_t ldpre, void* dP, int64_t lddp, float* scale, int dbias_type, void* dbias, void* workspace,
+                       int64_t workspace_bytes, void* stream);
+int64_t tgemm_linear_grad_f32_workspace(int64_t M, int64_t N, int64_t K, int type, int64_t ldx, int64_t ldw, int w_layout,
+                                        int act, int64_t lddy, int64_t lddx, int64_t lddw);
+int tgemm_linear_grad_f32(int64_t M, int64_t N, int64_t K, int type, const void* X, int64_t ldx, const void* W,
+                          int64_t ldw, int w_layout, int act, const void* pre, int64_t ldpre, const float* dY,
+                          int64_t lddy, void* dX, int64_t lddx, void* dW, int64_t lddw, int dbias_type, void* dbias,
+                          void* workspace, int64_t workspace_bytes, void* stream);
+
 /* Reduction of tgemm_xent's row losses. */
 enum { TGEMM_REDUCE_NONE = 0, TGEMM_REDUCE_SUM = 1, TGEMM_REDUCE_MEAN = 2 };
 

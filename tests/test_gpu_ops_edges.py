@@ -1,0 +1,159 @@
+"""The operators around the product where their definitions are strained:
+gradients in fp32, far pre-activations, long vocabularies, walks over several
+tiles, sizes past a launch's limits. Tolerances are sums of the method's own
+roundings, as in test_gpu_ops.py, whose helpers are used."""
+import pytest
+import torch
+
+import dense_tiled_gemm_tgemm_amd as tg
+from test_gpu_ops import (BF, F32, HF, U, act64, act_grad64, e_lse, forward64, half_step, rand, slope, tiny, within,
+                          xent64, xent_case, y_tol)
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------ fp32 gradients of an fp32 result --
+
+def rounded(got, ref, tol, what):
+    """within(), for results that their type may not hold: infinite where the value
+    lies past the type's largest one, either where it may."""
+    big = torch.finfo(got.dtype).max
+    g = got.detach().double().cpu()
+    past, near = ref.abs() - tol > big, ref.abs() + tol > big
+    assert (g[past] == torch.copysign(torch.full_like(ref, float("inf")), ref)[past]).all(), what
+    near = near & ((g.abs() == float("inf")) | past)
+    within(torch.where(near, ref, g), ref, tol, what)
+
+
+def check_f32_gradients(M, N, K, dtype, act, layout, bdt, sx, sw, sdy, seed=1):
+    """dx, dw, db of an fp32 result against the formula: dY is not rounded before
+    the activation's derivative and the column sums; dP is rounded once, in units
+    of its largest value (binary16: a step of 2^-24 of 2^14 at least)."""
+    print(f"f32 grad {M} {N} {K} {dtype} {act} {layout} {bdt} {sx} {sw} {sdy}", flush=True)
+    x, w, b = rand((M, K), seed, dtype, sx), rand((N, K), seed + 1, dtype, sw * K ** -0.5), rand((N,), seed + 2, bdt)
+    dy = rand((M, N), seed + 3, F32, sdy)
+    p, y64, e = forward64(x, w, b, act, None)
+    xd, wd = x.cuda().requires_grad_(), (w if layout == "NxK" else w.t().contiguous()).cuda().requires_grad_()
+    bd = b.cuda().requires_grad_()
+    y = tg.linear(xd, wd, bd, act, out_dtype=F32, w_layout=layout)
+    gx, gw, gb = torch.autograd.grad(y, [xd, wd, bd], dy.cuda())
+    h, d64 = half_step(dtype), dy.double()
+    dp = d64 * act_grad64(p, act)
+    ep = torch.zeros_like(dp)
+    if act != "none":
+        ep = d64.abs() * (slope(act) * (e + h * 1.01 * p.abs() + tiny(dtype)) + 2.0 ** -20)
+    er = ep + h * 1.01 * dp.abs() + tiny(dtype) * 2.0 ** -13 * float(d64.abs().max())
+    want = dp.sum(0)
+    rounded(gb, want, ep.sum(0) + (M + 4) * U * dp.abs().sum(0) + half_step(bdt) * 1.01 * want.abs() + tiny(bdt), "db")
+    want = dp @ w.double()
+    rounded(gx, want, 1.01 * (er @ w.double().abs()) + (N + 4) * U * (dp.abs() @ w.double().abs())
+           + h * 1.02 * want.abs() + tiny(dtype), "dx")
+    want = dp.t() @ x.double()
+    rounded(gw if layout == "NxK" else gw.t(), want, 1.01 * (er.t() @ x.double().abs())
+           + (M + 4) * U * (dp.abs().t() @ x.double().abs()) + h * 1.02 * want.abs() + tiny(dtype), "dw")
+
+
+@pytest.mark.parametrize("act", ["none", "silu", "gelu"])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_f32_gradient_keeps_its_range(act, dtype):
+    """Gradients below binary16's smallest step and above its largest value, and of mixed size."""
+    for sx, sw, sdy in ((300.0, 1 / 300, 1e-8), (1e-3, 1e-2, 1e5), (1.0, 1.0, 1.0)):
+        for M, N, K, lay in ((130, 300, 72, "NxK"), (5, 40, 24, "KxN"), (700, 136, 200, "KxN"), (64, 5, 3, "NxK"), (1, 1, 1, "NxK")):
+            check_f32_gradients(M, N, K, dtype, act, lay, F32 if M != 5 else dtype, sx, sw, sdy)
+
+
+def test_f32_gradient_of_a_mean():
+    """The mean of a large result: every gradient is 2^-26, below half of binary16's smallest step."""
+    M, N, K = 8192, 8192, 16
+    x, w = rand((M, K), 1, HF, 64.0).cuda().requires_grad_(), rand((N, K), 2, HF, 64.0).cuda().requires_grad_()
+    b = torch.zeros((N,), device="cuda", requires_grad=True)
+    gx, gw, gb = torch.autograd.grad(tg.linear(x, w, b, out_dtype=F32).mean(), [x, w, b])
+    assert torch.equal(gb, torch.full_like(gb, 2.0 ** -13))
+    for got, other in ((gx, w), (gw, x)):
+        s = other.detach().double()
+        want = (s.sum(0) * 2.0 ** -26)[None, :].expand(8192, K)
+        within(got, want.cpu(), (8196 * U * (s.abs().sum(0) * 2.0 ** -26)[None, :].cpu() + half_step(HF) * 1.01 * want.abs().cpu()
+                                 + tiny(HF)), "mean")
+
+
+def test_f32_gradient_special_values():
+    """Zeros; infinities and NaN stay in their rows of dx and columns of db, and do not set the scale."""
+    x, w = rand((70, 40), 1, HF).cuda().requires_grad_(), rand((50, 40), 2, HF).cuda().requires_grad_()
+    b = torch.zeros((50,), device="cuda", requires_grad=True)
+    y = tg.linear(x, w, b, act="silu", out_dtype=F32)
+    g = torch.autograd.grad(y, [x, w, b], torch.zeros((70, 50), device="cuda"), retain_graph=True)
+    assert all(t.abs().max() == 0 for t in g)
+    dy = rand((70, 50), 3, F32, 1e-6).cuda()
+    clean = torch.autograd.grad(y, [x, w, b], dy, retain_graph=True)
+    assert clean[0].abs().max() > 0
+    for bad in (float("inf"), float("nan")):
+        d2 = dy.clone()
+        d2[3, 7] = bad
+        gx, gw, gb = torch.autograd.grad(y, [x, w, b], d2, retain_graph=True)
+        keep = torch.arange(70) != 3
+        assert torch.equal(gx.cpu()[keep], clean[0].cpu()[keep]) and not gx[3].isfinite().any()
+        cols = torch.arange(50) != 7
+        assert torch.equal(gb.cpu()[cols], clean[2].cpu()[cols]) and not gb[7].isfinite()
+        assert torch.equal(gw.cpu()[cols], clean[1].cpu()[cols]) and not gw[7].isfinite().any()
+
+
+def test_f32_gradient_layouts_and_empty_operands():
+    """Broadcast, transposed and strided fp32 gradients; no rows; no columns; a residual's gradient."""
+    x, w = rand((50, 64), 1, HF).cuda().requires_grad_(), rand((40, 64), 2, HF).cuda().requires_grad_()
+    r = rand((50, 40), 3, HF).cuda().requires_grad_()
+    for act in ("none", "gelu"):
+        y = tg.linear(x, w, None, act, r, out_dtype=F32)
+        g1 = torch.autograd.grad(y, [x, w, r], torch.full((50, 40), 1e-3, device="cuda"), retain_graph=True)
+        g2 = torch.autograd.grad(y, [x, w, r], torch.full((40, 50), 1e-3, device="cuda").t(), retain_graph=True)
+        g3 = torch.autograd.grad(y, [x, w, r], torch.full((), 1e-3, device="cuda").expand(50, 40), retain_graph=True)
+        g4 = torch.autograd.grad(y, [x, w, r], torch.full((50, 47), 1e-3, device="cuda")[:, 3:43])
+        for g in (g2, g3, g4):
+            assert all(torch.equal(a, b) for a, b in zip(g1, g))
+        assert torch.equal(g1[2], torch.full_like(r, 1e-3))
+    b = torch.zeros((24,), device="cuda", requires_grad=True)
+    w = rand((24, 16), 1, HF).cuda().requires_grad_()
+    for act in ("none", "silu"):
+        x = torch.empty((0, 16), dtype=HF, device="cuda", requires_grad=True)
+        gx, gw, gb = torch.autograd.grad(tg.linear(x, w, b, act, out_dtype=F32), [x, w, b], torch.empty((0, 24), device="cuda"))
+        assert gx.shape == (0, 16) and gw.abs().max() == 0 and gb.abs().max() == 0
+        x = rand((5, 16), 3, HF).cuda().requires_grad_()
+        e = torch.empty((0, 16), dtype=HF, device="cuda", requires_grad=True)
+        gx, ge = torch.autograd.grad(tg.linear(x, e, act=act, out_dtype=F32), [x, e], torch.empty((5, 0), device="cuda"))
+        assert gx.abs().max() == 0 and ge.shape == (0, 16)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_act_grad_f32_entry(dtype):
+    """dP in units of *scale, the power of two that the largest |dY| sets in binary16;
+    only the column sums; nothing around the outputs is written."""
+    M, N = 133, 301
+    name = "bf16" if dtype == BF else "f16"
+    for size in (1e-30, 3e-9, 1.0, 7e8, 1e38):
+        dy, pre = rand((M, N), 1, F32).clamp(-3, 3) * size, rand((M, N), 2, dtype)
+        dyd, pd = dy.cuda(), pre.cuda()
+        for act in ("none", "gelu"):
+            dp = torch.full((M + 2, N + 7), 7.0, dtype=dtype, device="cuda")
+            db = torch.full((N + 4,), 7.0, device="cuda")
+            sc = torch.full((3,), 7.0, device="cuda")
+            need = tg.tgemm_act_grad_f32_workspace(M, N)
+            ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+            for only_db in (False, True):
+                rc = tg.tgemm_act_grad_f32(M, N, name, dyd.data_ptr(), N, act, None if act == "none" else pd.data_ptr(), N,
+                                           None if only_db else dp[1:].data_ptr(), N + 7,
+                                           None if only_db else sc[1:].data_ptr(), "f32", db[2:].data_ptr(), ws.data_ptr(),
+                                           need, torch.cuda.current_stream().cuda_stream)
+                assert rc == tg.TGEMM_OK
+                g = dy.double() * act_grad64(pre.double(), act)
+                slack = dy.double().abs() * 2.0 ** -20 * (act != "none")
+                want = g.sum(0)
+                if g.abs().sum(0).max() < torch.finfo(F32).max:      # (fp32 sums: their partial sums may overflow past that)
+                    within(db[2:2 + N], want, slack.sum(0) + (M + 4) * U * g.abs().sum(0) + 2 * U * want.abs(), "db")
+            scale = float(sc[1])
+            top = float(dy.abs().max())
+            assert scale == 1.0 if dtype == BF else (2.0 ** 14 <= top / scale < 2.0 ** 15)
+            assert torch.frexp(torch.tensor(scale))[0] == 0.5
+            within(dp[1:1 + M, :N].double() * scale, g, slack + half_step(dtype) * 1.01 * g.abs() + tiny(dtype) * scale, "dp")
+            dp[1:1 + M, :N] = 7.0
+            db[2:2 + N] = 7.0
+            sc[1] = 7.0
+            assert (dp == 7.0).all() and (db == 7.0).all() and (sc == 7.0).all()
