@@ -102,8 +102,13 @@ __device__ __forceinline__ float act_fwd(float x) {
     }
 }
 
+// The derivatives are 0 below -1000 and 1 above 1000 in fp32, and are taken
+// there: a pre-activation past 65504 is kept as an infinity in binary16, and the
+// square of one past 1.8e19 is one in bfloat16, where 0 * inf would come out.
 template <int ACT>
 __device__ __forceinline__ float act_grad(float x) {
+    if constexpr (ACT == kActSilu || ACT == kActGelu || ACT == kActGeluTanh)
+        x = __builtin_fabsf(x) > 1000.0f ? __builtin_copysignf(1000.0f, x) : x;   // (a NaN stays)
     if constexpr (ACT == kActRelu) {
         return x > 0.f ? 1.0f : (x <= 0.f ? 0.f : x);
     } else if constexpr (ACT == kActSilu) {

@@ -157,3 +157,27 @@ def test_act_grad_f32_entry(dtype):
             db[2:2 + N] = 7.0
             sc[1] = 7.0
             assert (dp == 7.0).all() and (db == 7.0).all() and (sc == 7.0).all()
+
+
+# ------------------------------------------- pre-activations far from zero --
+
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu", "gelu_tanh"])
+def test_gradient_of_far_preactivations(act):
+    """Derivatives are 0 far below zero and 1 far above, also where the kept
+    pre-activation has become infinite (binary16 past 65504) or its square does."""
+    for dtype, far in ((HF, (300.0, 6.5e4, 9e4, 2e5)), (BF, (300.0, 9e4, 1e19, 1e20, 1e38))):
+        for M in (3, 40):
+            x = torch.full((M, 1), 8.0, dtype=dtype)
+            v = torch.tensor(far + tuple(-f for f in far))
+            w = (v / 8).to(dtype)[:, None]
+            xd, wd = x.cuda().requires_grad_(), w.cuda().requires_grad_()
+            dy = torch.ones((M, len(v)), dtype=dtype, device="cuda")
+            gx, gw = torch.autograd.grad(tg.linear(xd, wd, act=act), [xd, wd], dy)
+            want = (w[:, 0].double() > 0).double()
+            assert torch.equal(gw.cpu()[:, 0].double(), want * 8 * M), (dtype, gw)
+            assert gx.isfinite().all()
+        # the call by itself
+        pre = torch.tensor([[float("inf"), -float("inf"), float("nan"), far[-1], -far[-1]]]).to(dtype).cuda()
+        dp, db = tg.act_grad(torch.ones((1, 5), dtype=dtype, device="cuda"), act, pre, F32)
+        assert dp[0, [0, 3]].eq(1).all() and dp[0, [1, 4]].eq(0).all() and dp[0, 2].isnan()
+        assert db[[0, 3]].eq(1).all() and db[[1, 4]].eq(0).all() and db[2].isnan()
