@@ -253,10 +253,12 @@ __global__ void __launch_bounds__(64) tgemm_xent_few_kernel(OpArgs a) {
             }
             const float top = fmaxf(mx[m], fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])));
             const float nm2 = -kLog2e * finite_max(top);
-            // (a running maximum of -inf comes with a sum of 0; one of +inf keeps its weight)
+            // (a running maximum of -inf comes with a sum of 0; one of +inf keeps its weight; one
+            // that stays keeps 1: taken through nm2, whose product is rounded, every group would
+            // multiply the sum by the same factor beside 1, 2e-4 of lse over 600,000 columns)
             const float keep = __builtin_fabsf(mx[m]) == __builtin_inff()
                                    ? 1.f
-                                   : __builtin_amdgcn_exp2f(__builtin_fmaf(kLog2e, mx[m], nm2));
+                                   : __builtin_amdgcn_exp2f(kLog2e * (mx[m] - finite_max(top)));
             float s = sum[m] * keep;
 #pragma unroll
             for (int e = 0; e < 4; ++e) s += __builtin_amdgcn_exp2f(__builtin_fmaf(kLog2e, z[e], nm2));

@@ -181,3 +181,59 @@ def test_gradient_of_far_preactivations(act):
         dp, db = tg.act_grad(torch.ones((1, 5), dtype=dtype, device="cuda"), act, pre, F32)
         assert dp[0, [0, 3]].eq(1).all() and dp[0, [1, 4]].eq(0).all() and dp[0, 2].isnan()
         assert db[[0, 3]].eq(1).all() and db[[1, 4]].eq(0).all() and db[2].isnan()
+
+
+# --------------------------------------- few rows over a long vocabulary --
+
+@pytest.mark.parametrize("R", [1, 5, 17, 32])
+def test_xent_few_rows_equal_logits_do_not_drift(R):
+    """All logits equal: lse = z + log V. A wave adds some twenty groups of columns,
+    four terms each, to its running sum, and the join some thirty parts: 125
+    roundings of 2^-24, those of the logarithm and of lse, and one rounding of
+    log2(e) z, the same in every term."""
+    V, D = 600_000, 8
+    for c in (360.0, -360.0, 412.0):     # where log2(e) c rounds by nearly half a step
+        h = torch.zeros((R, D), dtype=BF)
+        h[:, 0] = c
+        w = torch.zeros((V, D), dtype=BF)
+        w[:, 0] = 1
+        t = torch.full((R,), V - 1)
+        loss, lse = tg.linear_cross_entropy(h.cuda(), w.cuda(), t.cuda(), reduction="none", return_lse=True)
+        z = float(h[0, 0])
+        want = torch.full((R,), z, dtype=torch.float64) + torch.log(torch.tensor(float(V), dtype=torch.float64))
+        tol = 125 * U + 2 * U * want.abs() + U * 1.4427 * abs(z)
+        within(lse, want, tol, "lse")
+        within(loss, want - z, tol, "loss")
+
+
+@pytest.mark.parametrize("R", [1, 5, 17, 32])
+@pytest.mark.parametrize("V", [70_001, 150_000])
+@pytest.mark.parametrize("order", ["any", "rising", "falling"])
+def test_xent_few_rows_over_several_groups(R, V, order):
+    """More groups of columns than waves: the running maximum stays, rises or
+    falls from group to group, logits of hundreds; an infinite logit in a later group."""
+    D = 16
+    h, w, t = xent_case(R, V, D, BF, ignored=0.2, scale=40.0)
+    if order != "any":
+        z0 = (h[0].double() @ w.double().t())
+        w = w[torch.argsort(z0, descending=order == "falling")]
+    z, lse, loss, valid, ez = xent64(h, w, t)
+    got, gl = tg.linear_cross_entropy(h.cuda(), w.cuda(), t.cuda(), reduction="none", return_lse=True)
+    el = e_lse(lse, ez) + 2 * U * 1.4427 * z.abs().amax(1)
+    within(gl, lse, el, "lse")
+    within(got, loss, torch.where(valid, el + ez + U * loss.abs(), torch.zeros_like(el)), "loss")
+    # column V - 3 (a wave's last group): -inf drops out, +inf makes lse infinite
+    for v in (-float("inf"), float("inf")):
+        wi = w.clone()
+        hi = h.clone()
+        wi[:, 0] = 0
+        wi[V - 3, 0] = v
+        hi[:, 0] = 1
+        got = tg.linear_cross_entropy(hi.cuda(), wi.cuda(), t.cuda(), reduction="none", return_lse=True)[1]
+        if v > 0:
+            assert (got == float("inf")).all()
+        else:
+            z2 = hi[:, 1:].double() @ wi[:, 1:].double().t()
+            z2[:, V - 3] = v
+            l2 = torch.logsumexp(z2, 1)
+            within(got, l2, e_lse(l2, ez) + 2 * U * 1.4427 * z.abs().amax(1), "lse without the column")
