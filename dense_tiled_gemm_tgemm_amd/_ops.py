@@ -4,7 +4,9 @@
 As in ``_binding`` everything here marshals arguments; all arithmetic runs in
 the HIP kernels, on torch's current stream of the operands' device. Workspaces
 come from torch's allocator on that stream. ``linear`` and
-``linear_cross_entropy`` take part in autograd (first derivatives).
+``linear_cross_entropy`` take part in autograd (first derivatives, backward
+mode; operands with forward-mode tangents are refused, and so are torch.func's
+transforms).
 """
 from __future__ import annotations
 
@@ -223,6 +225,14 @@ def _device(t, name, like=None):
         raise ValueError(f"{name} must be a device tensor")
 
 
+def _no_tangents(torch, *operands):
+    """The functions have no forward-mode derivative: an operand that carries a
+    tangent is refused (a call without gradients would drop it)."""
+    fw = torch.autograd.forward_ad
+    if fw._current_level >= 0 and any(t is not None and fw.unpack_dual(t).tangent is not None for t in operands):
+        raise NotImplementedError("no forward-mode derivative: an operand carries a tangent")
+
+
 def _rows(t):
     """Row stride of a 2-D tensor that the kernels can read as it lies, or None:
     unit column stride and rows that do not overlap."""
@@ -342,7 +352,8 @@ def gemm_tn(A, B, out=None, out_dtype=None, alpha: float = 1.0, accumulate: bool
 
     out: optional (M, N) tensor with unit column stride, of A's dtype or
     float32; allocated as ``out_dtype`` (default A's dtype) when None. splits,
-    tile_m, k_step: explicit launch choices (tgemm_tn).
+    tile_m, k_step: explicit launch choices (tgemm_tn). A part of gradients: it
+    takes no part in autograd itself, its result has no history.
     """
     import torch
     if A.dim() != 2 or B.dim() != 2:
@@ -356,6 +367,7 @@ def gemm_tn(A, B, out=None, out_dtype=None, alpha: float = 1.0, accumulate: bool
     N = B.shape[1]
     if B.shape[0] != K:
         raise ValueError(f"the long axes differ: A is {tuple(A.shape)}, B is {tuple(B.shape)}")
+    _no_tangents(torch, A, B, out)
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
@@ -389,7 +401,8 @@ def gemm_tn(A, B, out=None, out_dtype=None, alpha: float = 1.0, accumulate: bool
 def act_grad(dy, act: str, pre=None, bias_dtype=None):
     """(dp, db): dp = dy * act'(pre) of dy's dtype (dy itself for "none"), and
     its column sums, taken before dp is rounded, as ``bias_dtype`` (dy's dtype
-    or float32; None: not computed). dy, pre: (M, N) float16 or bfloat16."""
+    or float32; None: not computed). dy, pre: (M, N) float16 or bfloat16. A part
+    of gradients: the results have no history in autograd."""
     import torch
     if act not in _ACTS:
         raise ValueError(f"act must be one of {sorted(_ACTS)}, got {act!r}")
@@ -401,6 +414,7 @@ def act_grad(dy, act: str, pre=None, bias_dtype=None):
     dev = dy.device
     if bias_dtype not in (None, dy.dtype, torch.float32):
         raise TypeError(f"bias_dtype must be {dy.dtype} or float32, got {bias_dtype}")
+    _no_tangents(torch, dy)
     dy, lddy = _readable(dy)
     pre_ptr = dp_ptr = None
     ldpre = lddp = 0
@@ -410,6 +424,7 @@ def act_grad(dy, act: str, pre=None, bias_dtype=None):
             if pre is None or tuple(pre.shape) != (M, N) or pre.dtype != dy.dtype:
                 raise ValueError(f"pre must be a ({M}, {N}) {dy.dtype} tensor")
             _device(pre, "pre", dev)
+            _no_tangents(torch, pre)
             pre, ldpre = _readable(pre)
             dp = torch.empty((M, N), dtype=dy.dtype, device=dev)
             lddp = max(N, 1)
@@ -542,6 +557,7 @@ def linear(x, weight, bias=None, act: str = "none", residual=None, out_dtype=Non
         if residual.shape != shape or residual.dtype != dt:
             raise ValueError(f"residual must be a {tuple(shape)} tensor of {dt}")
         _device(residual, "residual", dev)
+    _no_tangents(torch, x, weight, bias, residual)
     if x.dim() != 2:
         rows = 1
         for s in x.shape[:-1]:
@@ -720,6 +736,7 @@ def linear_cross_entropy(hidden, weight, target, ignore_index: int = -100, reduc
     if target.dtype != torch.int64 or target.shape != shape:
         raise ValueError(f"target must be a {tuple(shape)} int64 tensor")
     _device(target, "target", dev)
+    _no_tangents(torch, hidden, weight)
     rows = target.numel()
     if rows == 0 and reduction != "none":
         raise ValueError("a reduction over no rows")

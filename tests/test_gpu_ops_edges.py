@@ -237,3 +237,28 @@ def test_xent_few_rows_over_several_groups(R, V, order):
             z2[:, V - 3] = v
             l2 = torch.logsumexp(z2, 1)
             within(got, l2, e_lse(l2, ez) + 2 * U * 1.4427 * z.abs().amax(1), "lse without the column")
+
+
+# ------------------------------------------------- forward-mode tangents --
+
+def test_forward_mode_is_refused_and_not_dropped():
+    """A tangent of any operand raises; none is lost without a word."""
+    import torch.autograd.forward_ad as fw
+    x, w, b, r = (rand(s, i, BF).cuda() for i, s in enumerate(((4, 16), (24, 16), (24,), (4, 24))))
+    t = torch.tensor([1, 2, -100, 3]).cuda()
+    calls = {"linear": lambda x, w, b, r: tg.linear(x, w, b, "silu", r),
+             "xent": lambda x, w, b, r: tg.linear_cross_entropy(x, w, t),
+             "tn": lambda x, w, b, r: tg.gemm_tn(x, r),
+             "act_grad": lambda x, w, b, r: tg.act_grad(r, "silu", r)}
+    uses = {"linear": (0, 1, 2, 3), "xent": (0, 1), "tn": (0, 3), "act_grad": (3,)}
+    for name, call in calls.items():
+        for i in uses[name]:
+            for leaf in (False, True):
+                ops = [q.clone().requires_grad_(leaf) for q in (x, w, b, r)]
+                with fw.dual_level():
+                    ops[i] = fw.make_dual(ops[i], torch.ones_like(ops[i]))
+                    with pytest.raises(NotImplementedError, match="forward-mode"):
+                        call(*ops)
+    with fw.dual_level():                            # operands without tangents are served inside a level too
+        a = tg.linear(x, w, b, "silu", r)
+    assert torch.equal(a, tg.linear(x, w, b, "silu", r))
