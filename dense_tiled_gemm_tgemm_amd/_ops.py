@@ -255,6 +255,15 @@ def _readable(t):
     return t, ld
 
 
+# Rows of the cross entropy's operands lie at most this many elements apart.
+_MAX_LD = 4000000
+
+
+def _near(t):
+    """t, or a contiguous copy where its rows lie further apart than _MAX_LD."""
+    return t.contiguous() if (_rows(t) or 0) > _MAX_LD else t
+
+
 class _Here:
     """The device is the current one already."""
     def __enter__(self):
@@ -294,7 +303,7 @@ def _linear(torch, x, w, bias, act, residual, out_dtype, layout, keep_pre, tile_
         ldr = 0
         if residual is not None:
             residual, ldr = _readable(residual)
-            if ldr > 4000000:
+            if ldr > _MAX_LD:
                 residual, ldr = residual.contiguous(), ldy
         ws, ws_ptr = _alloc(torch, need, dev)
         b_code = TGEMM_F32
@@ -740,7 +749,8 @@ def linear_cross_entropy(hidden, weight, target, ignore_index: int = -100, reduc
     rows = target.numel()
     if rows == 0 and reduction != "none":
         raise ValueError("a reduction over no rows")
-    h = hidden if hidden.dim() == 2 else hidden.reshape(rows, D)
+    h = _near(hidden if hidden.dim() == 2 else hidden.reshape(rows, D))
+    weight = _near(weight)
     t = target.reshape(rows)
     if torch.is_grad_enabled() and (h.requires_grad or weight.requires_grad):
         both = not recompute and not return_lse and reduction != "none" and _both_ok(torch, h, weight)

@@ -162,7 +162,9 @@ enum { TGEMM_REDUCE_NONE = 0, TGEMM_REDUCE_SUM = 1, TGEMM_REDUCE_MEAN = 2 };
  * for SUM and MEAN, NULL for NONE. A target outside the vocabulary that is not
  * `ignore` gives a loss of NaN; it is never used as an index.
  * dim >= 8, rows and vocab >= 1 (rows == 0 does nothing; SUM and MEAN then
- * return TGEMM_ERR_INVALID). vocab * 4 bytes must fit in 31 bits.
+ * return TGEMM_ERR_INVALID). vocab * 4 bytes must fit in 31 bits. Rows of H and W
+ * (and of dH and dW in the calls below) lie at most 4,000,000 elements apart,
+ * TGEMM_ERR_UNSUPPORTED otherwise.
  */
 int64_t tgemm_xent_workspace(int64_t rows, int64_t vocab, int64_t dim, int type, int64_t ldh, int64_t ldw);
 int tgemm_xent(int64_t rows, int64_t vocab, int64_t dim, int type, const void* H, int64_t ldh, const void* W,

@@ -262,3 +262,29 @@ def test_forward_mode_is_refused_and_not_dropped():
     with fw.dual_level():                            # operands without tangents are served inside a level too
         a = tg.linear(x, w, b, "silu", r)
     assert torch.equal(a, tg.linear(x, w, b, "silu", r))
+
+
+# ------------------------------------------ row strides and vocabularies --
+
+@pytest.mark.parametrize("R", [4, 40])
+def test_xent_long_strides_are_copied(R):
+    """Rows further apart than the kernels' offsets reach give the same results as contiguous ones."""
+    ld, D, V = 4_000_008, 64, 30
+    h, w, t = xent_case(R, V, D, BF, ignored=0.0)
+    buf = torch.empty(R * ld, dtype=BF, device="cuda")
+    hl = buf.as_strided((R, D), (ld, 1))
+    hl.copy_(h.cuda())
+    if R > V:                                        # (the buffer holds as many rows)
+        wl = buf.as_strided((V, D), (ld, 1), 1024)
+        wl.copy_(w.cuda())
+    for kw in ({"reduction": "none"}, {}, {"recompute": True}):
+        def both(h, w):
+            hd, wd = h.detach().requires_grad_(), w.detach().requires_grad_()
+            out = tg.linear_cross_entropy(hd, wd, t.cuda(), **kw)
+            return (out.detach(),) + torch.autograd.grad(out.sum(), [hd, wd])
+        want = both(h.cuda(), w.cuda())
+        for ops in ((hl, w.cuda()),) + (((h.cuda(), wl), (hl, wl)) if R > V else ()):
+            got = both(*ops)
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert torch.equal(tg.linear_cross_entropy(hl, w.cuda(), t.cuda(), reduction="none"),
+                           tg.linear_cross_entropy(h.cuda(), w.cuda(), t.cuda(), reduction="none"))
