@@ -709,7 +709,7 @@ def linear_cross_entropy(hidden, weight, target, ignore_index: int = -100, reduc
     hidden: (..., D) and weight: (V, D), float16 or bfloat16 device tensors, D >=
     8; target: (...) int64. Rows whose target is ``ignore_index`` have loss 0 and
     pass no gradient. reduction: "none" (float32 losses of target's shape),
-    "sum" or "mean" (over the rows that are not ignored; 0 where all are).
+    "sum" or "mean" (over the rows that are not ignored; 0 where there is none).
     return_lse: also the rows' log-sum-exp, float32 of target's shape
     (differentiable: a penalty on it needs no second pass).
 
@@ -748,7 +748,9 @@ def linear_cross_entropy(hidden, weight, target, ignore_index: int = -100, reduc
     _no_tangents(torch, hidden, weight)
     rows = target.numel()
     if rows == 0 and reduction != "none":
-        raise ValueError("a reduction over no rows")
+        # the sum over no rows (a mean divides by one at least)
+        loss, lse = linear_cross_entropy(hidden, weight, target, ignore_index, "none", True)
+        return (loss.sum(), lse) if return_lse else loss.sum()
     h = _near(hidden if hidden.dim() == 2 else hidden.reshape(rows, D))
     weight = _near(weight)
     t = target.reshape(rows)

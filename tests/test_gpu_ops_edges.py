@@ -288,3 +288,21 @@ def test_xent_long_strides_are_copied(R):
             assert all(torch.equal(a, b) for a, b in zip(got, want))
         assert torch.equal(tg.linear_cross_entropy(hl, w.cuda(), t.cuda(), reduction="none"),
                            tg.linear_cross_entropy(h.cuda(), w.cuda(), t.cuda(), reduction="none"))
+
+
+@pytest.mark.parametrize("reduction", ["sum", "mean"])
+def test_xent_reduction_over_no_rows(reduction):
+    """A sum over no rows is 0 (a mean divides by one at least), its gradients are zeros."""
+    w = rand((30, 16), 1, BF).cuda().requires_grad_()
+    h = torch.empty((0, 16), dtype=BF, device="cuda", requires_grad=True)
+    t = torch.empty((0,), dtype=torch.int64, device="cuda")
+    for kw in ({}, {"recompute": True}, {"return_lse": True}):
+        loss = tg.linear_cross_entropy(h, w, t, reduction=reduction, **kw)
+        if kw.get("return_lse"):
+            loss, lse = loss
+            assert lse.shape == (0,)
+        assert loss.shape == () and loss.dtype == F32 and loss.item() == 0
+        gh, gw = torch.autograd.grad(loss, [h, w])
+        assert gh.shape == (0, 16) and gw.shape == w.shape and gw.abs().max() == 0
+    with torch.no_grad():
+        assert tg.linear_cross_entropy(h, w, t, reduction=reduction).item() == 0
