@@ -168,7 +168,10 @@ int plan_product(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int 
         return TGEMM_OK;
     }
     const bool few = few_ok && nxk && !akm && M <= kFewMost && lda <= kMaxDmaLd && ldb <= kMaxDmaLd;
-    const bool tile = lda >= 8 && ldb >= 8 && lda <= kMaxDmaLd && ldb <= kMaxDmaLd && N <= kMaxDmaLd;
+    // (N bounds the row stride of the fp32 sums, which a product in one part that
+    // its own end of tile finishes does not have)
+    const bool tile = lda >= 8 && ldb >= 8 && lda <= kMaxDmaLd && ldb <= kMaxDmaLd &&
+                      (N <= kMaxDmaLd || (direct && one_part));
     if ((tile_m == 16 && !few) || (tile_m > 16 && !tile)) return TGEMM_ERR_UNSUPPORTED;
     if (few && (tile_m == 16 || (tile_m == 0 && k_step == 0 && splits <= 1 && M <= kFewRows))) {
         if (splits > 1) return TGEMM_ERR_UNSUPPORTED;

@@ -306,3 +306,37 @@ def test_xent_reduction_over_no_rows(reduction):
         assert gh.shape == (0, 16) and gw.shape == w.shape and gw.abs().max() == 0
     with torch.no_grad():
         assert tg.linear_cross_entropy(h, w, t, reduction=reduction).item() == 0
+
+
+@pytest.mark.parametrize("R", [5, 40])
+def test_xent_vocabulary_past_four_million(R):
+    """More columns than an operand's row may have elements: the columns are rows of the weight."""
+    V, D = 4_000_037, 8
+    g = torch.Generator(device="cuda").manual_seed(3)
+    h = torch.randn((R, D), generator=g, device="cuda").to(BF).requires_grad_()
+    w = (torch.randn((V, D), generator=g, device="cuda") * 0.5).to(BF).requires_grad_()
+    t = torch.randint(0, V, (R,), generator=g, device="cuda")
+    t[1], t[2], t[3] = V - 1, 4_000_000, -100
+    loss, lse = tg.linear_cross_entropy(h, w, t, reduction="none", return_lse=True)
+    gh, gw = torch.autograd.grad(loss.sum(), [h, w])
+    hd, wd = h.detach().double(), w.detach().double()
+    z = hd @ wd.t()
+    l64 = torch.logsumexp(z, 1)
+    zt = z.gather(1, t.clamp(min=0)[:, None])[:, 0]
+    live = (t >= 0).double()
+    ez = ((D + 4) * U * (hd.abs() @ wd.abs().t()).amax(1)).cpu()
+    el = e_lse(l64.cpu(), ez)
+    within(lse, l64.cpu(), el, "lse")
+    within(loss, ((l64 - zt) * live).cpu(), (el + ez + U * (l64 - zt).abs().cpu()) * live.cpu() , "loss")
+    # z becomes the coefficients
+    z.sub_(l64[:, None]).exp_().mul_(live[:, None])
+    z[torch.arange(R, device="cuda"), t.clamp(min=0)] -= live
+    want = z @ wd
+    rel = (half_step(BF) * 1.02 + (2 * ez + 2.0 ** -18).cuda())[:, None]
+    tol = (rel * z.abs() + 4 * U * (z.abs() > 0.5)) @ wd.abs() + (V + 4) * U * (z.abs() @ wd.abs()) + half_step(BF) * 1.02 * want.abs()
+    within(gh, want.cpu(), tol.cpu(), "dh")
+    cols = torch.cat([torch.tensor([0, 1, 3_999_999, 4_000_000, 4_000_001, V - 2, V - 1], device="cuda"), t[t >= 0]])
+    want = z[:, cols].t() @ hd
+    tol = ((rel * z.abs() + 4 * U * (z.abs() > 0.5))[:, cols].t() @ hd.abs() + (R + 4) * U * (z[:, cols].abs().t() @ hd.abs())
+           + half_step(BF) * 1.02 * want.abs())
+    within(gw[cols], want.cpu(), tol.cpu(), "dw")
