@@ -255,7 +255,7 @@ def _readable(t):
     return t, ld
 
 
-# Rows of the cross entropy's operands lie at most this many elements apart.
+# Rows of the cross entropy's operands and of a residual lie at most this many elements apart.
 _MAX_LD = 4000000
 
 
@@ -303,7 +303,7 @@ def _linear(torch, x, w, bias, act, residual, out_dtype, layout, keep_pre, tile_
         ldr = 0
         if residual is not None:
             residual, ldr = _readable(residual)
-            if ldr > _MAX_LD:
+            if ldr > _MAX_LD >= N:
                 residual, ldr = residual.contiguous(), ldy
         ws, ws_ptr = _alloc(torch, need, dev)
         b_code = TGEMM_F32

@@ -619,7 +619,8 @@ int linear_call(int64_t M, int64_t N, int64_t K, int type, const void* X, int64_
     if (meet(mp, mx) || meet(mp, mw) || meet(mp, mb) || meet(mp, mr)) return TGEMM_ERR_INVALID;
     OpPlan pl;
     int ncu;
-    if ((residual && ldr > kMaxDmaLd) || (pre && ldpre > kMaxDmaLd)) return TGEMM_ERR_UNSUPPORTED;
+    // (longer rows than that never run on tiles, whose offsets the limit is for)
+    if (N <= kMaxDmaLd && ((residual && ldr > kMaxDmaLd) || (pre && ldpre > kMaxDmaLd))) return TGEMM_ERR_UNSUPPORTED;
     int rc = plan_linear(M, N, K, type, ldx, ldw, w_layout, y_type, ldy, tile_m, k_step, splits, &ncu, &pl);
     if (rc != TGEMM_OK) return rc;
     if (!ws_ok(workspace, workspace_bytes, pl.ws)) return TGEMM_ERR_INVALID;

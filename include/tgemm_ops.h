@@ -51,7 +51,8 @@ enum { TGEMM_ACT_SILU = 2, TGEMM_ACT_GELU = 3, TGEMM_ACT_GELU_TANH = 4 };
  *        values the activation's derivative is taken at, in return for half the
  *        bytes kept from the forward to the backward pass.
  * Rows of the residual and of pre lie at most 4,000,000 elements apart
- * (TGEMM_ERR_UNSUPPORTED otherwise); X, W and Y may have any stride.
+ * (TGEMM_ERR_UNSUPPORTED otherwise), or at any distance where N is more than
+ * that; X, W and Y may have any stride.
  * In fp32 after the fp32 sums: v = alpha * sum + bias (one fused multiply-add),
  * v = act(v) + residual, one rounding to y_type.
  * K == 0: the sums are zero. M == 0 or N == 0: nothing is done.

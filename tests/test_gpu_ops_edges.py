@@ -340,3 +340,28 @@ def test_xent_vocabulary_past_four_million(R):
     tol = ((rel * z.abs() + 4 * U * (z.abs() > 0.5))[:, cols].t() @ hd.abs() + (R + 4) * U * (z[:, cols].abs().t() @ hd.abs())
            + half_step(BF) * 1.02 * want.abs())
     within(gw[cols], want.cpu(), tol.cpu(), "dw")
+
+
+@pytest.mark.parametrize("M", [1, 3, 40])
+def test_linear_of_more_than_four_million_columns(M):
+    """A residual and a kept pre-activation whose rows are longer than the tiles'
+    offsets reach: those sizes do not run on tiles."""
+    N, K = 4_000_003, 8
+    g = torch.Generator(device="cuda").manual_seed(M)
+    x = torch.randn((M, K), generator=g, device="cuda").to(BF).requires_grad_()
+    w = (torch.randn((N, K), generator=g, device="cuda") * 0.4).to(BF).requires_grad_()
+    r = torch.randn((M, N), generator=g, device="cuda").to(BF).requires_grad_()
+    y = tg.linear(x, w, None, "silu", r)
+    xs, ws, rs = x.detach().cpu(), w.detach().cpu(), r.detach().cpu()
+    p, ref, e = forward64(xs, ws, None, "silu", rs)
+    within(y, ref, y_tol(p, ref, e, BF, rs), "y")
+    dy = torch.randn((M, N), generator=g, device="cuda").to(BF)
+    gx, gw, gr = torch.autograd.grad(y, [x, w, r], dy)
+    assert torch.equal(gr, dy)
+    h, d64 = half_step(BF), dy.double().cpu()
+    dp = d64 * act_grad64(p, "silu")
+    er = 1.01 * h * dp.abs() + 1.01 * d64.abs() * (1.2 * (e + h * 1.01 * p.abs()) + 2.0 ** -20)
+    want = dp.t() @ xs.double()
+    within(gw, want, er.t() @ xs.double().abs() + (M + 4) * U * (dp.abs().t() @ xs.double().abs()) + h * 1.02 * want.abs(), "dw")
+    want = dp @ ws.double()
+    within(gx, want, er @ ws.double().abs() + (N + 4) * U * (dp.abs() @ ws.double().abs()) + h * 1.02 * want.abs(), "dx")
