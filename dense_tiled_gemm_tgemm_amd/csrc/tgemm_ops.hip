@@ -19,12 +19,16 @@ constexpr int64_t kMaxDim = 2147483647;
 constexpr int kFewRows = 32;                // rows of X that a workgroup of the few-rows kernels takes
 constexpr int kFewMost = 1024;              // the most rows, in such blocks
 constexpr int kMaxSplits = 64;
+constexpr int64_t kMaxThreads = (int64_t(1) << 32) - 1;   // of one launch along a grid's axis
+constexpr int64_t kFewCols = int64_t(1) << 26;            // columns of one launch of the few-rows kernel
 enum : int { kPathNone = 0, kPathFew, kPathTile, kPathGeneral, kPathEmpty };
 
 int esize(int t) { return t == TGEMM_F32 ? 4 : 2; }
 bool is16(int t) { return t == TGEMM_F16 || t == TGEMM_BF16; }
 int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+// Workgroups of the row and column joins, which take the rest in turn.
+int64_t join_grid(int64_t n) { return n < (1 << 20) ? n : 1 << 20; }
 
 // Row stride of the cross entropy's coefficients: whole 128-byte lines, an odd
 // number of them, so that the rows a K step reads of one column range spread
@@ -200,6 +204,7 @@ int plan_product(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int 
             fit_splits(K, s, ks, &sp, &per);
             if (!splits && sp != s && s > 1) continue;
             const bool join = sp > 1 || !direct;
+            if (ceil_div(M, tm) * ceil_div(N, 256) * sp * NTHREADS > kMaxThreads) continue;
             const double t = tile_time(M, N, per, tm, ks, akm ? 2 : (nxk ? 0 : 1), sp, ncu, join,
                                        lda % 8 != 0 || ldb % 8 != 0);
             if (best == 0 || t < best) {
@@ -212,7 +217,11 @@ int plan_product(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int 
             }
         }
     }
-    if (best == 0) return TGEMM_ERR_UNSUPPORTED;
+    if (best == 0) {
+        // (no choice, or, past a billion rows, no grid that one launch takes)
+        if (tile_m || k_step || splits > 1 || one_part) return TGEMM_ERR_UNSUPPORTED;
+        return plan_product(M, N, K, lda, ldb, nxk, akm, direct, one_part, few_ok, 1, 0, 0, ncu, pl);
+    }
     if (few && !tile_m && !k_step && splits <= 1 && few_time(M, N, K, ncu, lda % 8 != 0 || ldb % 8 != 0) < best) {
         *pl = OpPlan{};
         pl->splits = 1;
@@ -331,13 +340,27 @@ int run_linear(OpArgs& a, int ab, int nxk, bool c32, int type, const OpPlan& pl,
         // waves along K: eight, or four where there are few pieces of 128 (1 x
         // 12288 x 512: 5.4 us with four, 6.4 with eight; 1 x 8192 x 4096: 16.6
         // and 14.6)
-        const int64_t wgs = ceil_div(a.N, 16);
         const bool four = a.K <= 4 * kFewK;
         int c = c32;
-        void* kargs[] = {&a, &c};
         const void* fn = four ? (ab ? few_kernel<1, 4>(a.M) : few_kernel<0, 4>(a.M))
                               : (ab ? few_kernel<1, 8>(a.M) : few_kernel<0, 8>(a.M));
-        return launch_k(fn, wgs, a.M <= 16 ? 1 : ceil_div(a.M, kFewRows), four ? 256 : 512, kargs, stream);
+        const int64_t N = a.N;
+        const OpArgs all = a;
+        for (int64_t n0 = 0; n0 < N; n0 += kFewCols) {
+            auto at = [n0](const void* p, int es) { return p ? static_cast<const char*>(p) + n0 * es : nullptr; };
+            OpArgs q = all;
+            q.N = (int)(N - n0 < kFewCols ? N - n0 : kFewCols);
+            q.B = all.B + n0 * all.ldb;
+            q.C = const_cast<char*>(at(all.C, c32 ? 4 : 2));
+            q.biasv = at(all.biasv, all.bias_f32 ? 4 : 2);
+            q.res = at(all.res, 2);
+            q.pre = const_cast<char*>(at(all.pre, 2));
+            void* kargs[] = {&q, &c};
+            const int rc = launch_k(fn, ceil_div(q.N, 16), a.M <= 16 ? 1 : ceil_div(a.M, kFewRows), four ? 256 : 512, kargs,
+                                    stream);
+            if (rc != TGEMM_OK) return rc;
+        }
+        return TGEMM_OK;
     }
     float* sums = static_cast<float*>(ws);
     if (pl.path == kPathTile && !pl.join) return launch_tile(a, ab, c32 ? kEndLin32 : kEndLin16, a.act, nxk, 0, pl, ncu, stream);
@@ -472,7 +495,7 @@ int xent_finish(const OpArgs& a, int64_t nparts, int64_t vocab, int64_t ignore, 
         void* kargs[] = {&part, &parts, &r, &zt, &target, &vocab, &ignore, &lse, &loss, &recs};
         const bool wide = r >= 512;
         const int rc = launch_k(wide ? (const void*)&tgemm_xent_join_kernel<16> : (const void*)&tgemm_xent_join_kernel<2>,
-                                ceil_div(r, wide ? 16 : 2), 1, 256, kargs, stream);
+                                join_grid(ceil_div(r, wide ? 16 : 2)), 1, 256, kargs, stream);
         if (rc != TGEMM_OK || reduction == TGEMM_REDUCE_NONE) return rc;
     }
     int mean = reduction == TGEMM_REDUCE_MEAN;
@@ -804,7 +827,7 @@ int act_grad_call(int64_t M, int64_t N, int type, bool f32, const void* dY, int6
     const float* cpart = part;
     void* kargs[] = {&cpart, &nb, &n, &dbias, &out32};
     return launch_k(ab ? (const void*)&tgemm_colsum_join_kernel<1> : (const void*)&tgemm_colsum_join_kernel<0>,
-                    ceil_div(N, 64), 1, 256, kargs, stream);
+                    join_grid(ceil_div(N, 64)), 1, 256, kargs, stream);
 }
 
 }  // namespace

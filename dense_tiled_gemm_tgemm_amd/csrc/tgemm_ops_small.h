@@ -538,22 +538,25 @@ template <int AB>
 __global__ void __launch_bounds__(256) tgemm_colsum_join_kernel(const float* part, int blocks, int N, void* out, int out_f32) {
     __shared__ float red[4][64];
     const int c = threadIdx.x & 63, q = threadIdx.x >> 6;
-    const int col = (int)blockIdx.x * 64 + c;
     const int per = (blocks + 3) / 4;
     const int b1 = (q + 1) * per < blocks ? (q + 1) * per : blocks;
-    float s = 0.f;
-    if (col < N) {
+    for (int64_t c0 = (int64_t)blockIdx.x * 64; c0 < N; c0 += (int64_t)gridDim.x * 64) {
+        const int64_t col = c0 + c;
+        float s = 0.f;
+        if (col < N) {
 #pragma unroll 8
-        for (int b = q * per; b < b1; ++b) s += part[(int64_t)b * N + col];
-    }
-    red[q][c] = s;
-    __syncthreads();
-    if (q == 0 && col < N) {
-        s = (red[0][c] + red[1][c]) + (red[2][c] + red[3][c]);
-        if (out_f32)
-            static_cast<float*>(out)[col] = s;
-        else
-            static_cast<uint16_t*>(out)[col] = to16<AB>(s);
+            for (int b = q * per; b < b1; ++b) s += part[(int64_t)b * N + col];
+        }
+        red[q][c] = s;
+        __syncthreads();
+        if (q == 0 && col < N) {
+            s = (red[0][c] + red[1][c]) + (red[2][c] + red[3][c]);
+            if (out_f32)
+                static_cast<float*>(out)[col] = s;
+            else
+                static_cast<uint16_t*>(out)[col] = to16<AB>(s);
+        }
+        __syncthreads();
     }
 }
 
@@ -572,49 +575,52 @@ tgemm_xent_join_kernel(const float2* part, int parts, int rows, const float* zt,
     constexpr int kQ = 256 / RW;
     __shared__ float sm[kQ][RW], ss[kQ][RW];
     const int r = threadIdx.x % RW, q = threadIdx.x / RW;
-    const int row = (int)blockIdx.x * RW + r;
-    float m = -__builtin_inff(), s = 0.f;
-    auto add = [&](float pm, float ps) {
-        const float top = fmaxf(m, pm), f = finite_max(top);
-        const float wm = __builtin_fabsf(m) == __builtin_inff() ? 1.f : __builtin_amdgcn_exp2f(kLog2e * (m - f));
-        const float wp = __builtin_fabsf(pm) == __builtin_inff() ? 1.f : __builtin_amdgcn_exp2f(kLog2e * (pm - f));
-        s = s * wm + ps * wp;
-        m = top;
-    };
-    if (row < rows) {
+    for (int64_t row0 = (int64_t)blockIdx.x * RW; row0 < rows; row0 += (int64_t)gridDim.x * RW) {
+        const int64_t row = row0 + r;
+        float m = -__builtin_inff(), s = 0.f;
+        auto add = [&](float pm, float ps) {
+            const float top = fmaxf(m, pm), f = finite_max(top);
+            const float wm = __builtin_fabsf(m) == __builtin_inff() ? 1.f : __builtin_amdgcn_exp2f(kLog2e * (m - f));
+            const float wp = __builtin_fabsf(pm) == __builtin_inff() ? 1.f : __builtin_amdgcn_exp2f(kLog2e * (pm - f));
+            s = s * wm + ps * wp;
+            m = top;
+        };
+        if (row < rows) {
 #pragma unroll 4
-        for (int p = q; p < parts; p += kQ) {
-            const float2 v = part[(int64_t)p * rows + row];
-            add(v.x, v.y);
+            for (int p = q; p < parts; p += kQ) {
+                const float2 v = part[(int64_t)p * rows + row];
+                add(v.x, v.y);
+            }
         }
-    }
-    sm[q][r] = m;
-    ss[q][r] = s;
+        sm[q][r] = m;
+        ss[q][r] = s;
 #pragma unroll
-    for (int o = kQ / 2; o; o >>= 1) {
+        for (int o = kQ / 2; o; o >>= 1) {
+            __syncthreads();
+            if (q < o) {
+                add(sm[q + o][r], ss[q + o][r]);
+                sm[q][r] = m;
+                ss[q][r] = s;
+            }
+        }
+        if (q == 0 && row < rows) {
+            const float l = finite_max(m) + logf(s);
+            lse[row] = l;
+            const int64_t t = target[row];
+            float v = 0.f;
+            const bool live = t != ignore, bad = live && (t < 0 || t >= V);
+            if (live) v = bad ? __builtin_nanf("") : l - zt[row];
+            loss[row] = v;
+            if (recs) {
+                XentRow x;
+                x.nl2 = -kLog2e * l;
+                x.p = bad ? __builtin_nanf("") : (live ? 1.0f : 0.f);
+                x.hot = live ? 1.0f : 0.f;
+                x.target = live && !bad ? (int)t : -1;
+                recs[row] = x;
+            }
+        }
         __syncthreads();
-        if (q < o) {
-            add(sm[q + o][r], ss[q + o][r]);
-            sm[q][r] = m;
-            ss[q][r] = s;
-        }
-    }
-    if (q == 0 && row < rows) {
-        const float l = finite_max(m) + logf(s);
-        lse[row] = l;
-        const int64_t t = target[row];
-        float v = 0.f;
-        const bool live = t != ignore, bad = live && (t < 0 || t >= V);
-        if (live) v = bad ? __builtin_nanf("") : l - zt[row];
-        loss[row] = v;
-        if (recs) {
-            XentRow r;
-            r.nl2 = -kLog2e * l;
-            r.p = bad ? __builtin_nanf("") : (live ? 1.0f : 0.f);
-            r.hot = live ? 1.0f : 0.f;
-            r.target = live && !bad ? (int)t : -1;
-            recs[row] = r;
-        }
     }
 }
 

@@ -365,3 +365,38 @@ def test_linear_of_more_than_four_million_columns(M):
     within(gw, want, er.t() @ xs.double().abs() + (M + 4) * U * (dp.abs().t() @ xs.double().abs()) + h * 1.02 * want.abs(), "dw")
     want = dp @ ws.double()
     within(gx, want, er @ ws.double().abs() + (N + 4) * U * (dp.abs() @ ws.double().abs()) + h * 1.02 * want.abs(), "dx")
+
+
+# --------------------------------------------- sizes past one launch's grid --
+
+def test_few_rows_of_more_columns_than_one_grid():
+    """2^27 columns and a ragged end: past 2^32 threads in one launch of 16 columns a workgroup."""
+    N, K = 2 ** 27 + 5, 1
+    g = torch.Generator(device="cuda").manual_seed(1)
+    w = torch.randint(-8, 9, (N, K), generator=g, device="cuda", dtype=torch.int8).to(BF)
+    b = torch.randint(-8, 9, (N,), generator=g, device="cuda", dtype=torch.int8).to(BF)
+    for M in (1, 2):
+        x = torch.full((M, K), 2.0, dtype=BF, device="cuda")
+        y = tg.linear(x, w, b, "relu")
+        for i in range(M):
+            assert torch.equal(y[i], (w[:, 0] * 2 + b).clamp(min=0))     # small whole numbers: exact
+
+
+def test_column_sums_of_more_columns_than_one_grid():
+    N = 2 ** 30 + 3
+    dy = torch.randint(-8, 9, (1, N), device="cuda", dtype=torch.int8).to(BF)
+    dp, db = tg.act_grad(dy, "none", None, BF)
+    assert torch.equal(db, dy[0])
+
+
+def test_xent_of_more_rows_than_one_grid():
+    """2^28 rows and a ragged end of a vocabulary of one: lse is the logit, the loss 0."""
+    R = 2 ** 28 + 21
+    h = torch.randint(-8, 9, (R, 8), device="cuda", dtype=torch.int8).to(BF)
+    w = torch.zeros((1, 8), dtype=BF, device="cuda")
+    w[0, 3] = 1
+    t = torch.zeros((R,), dtype=torch.int64, device="cuda")
+    loss, lse = tg.linear_cross_entropy(h, w, t, reduction="none", return_lse=True)
+    # (the exponential against the maximum is one step of log2(e) z away from 1)
+    z = h[:, 3].float()
+    assert ((lse - z).abs() <= e_lse(z, 0.0)).all() and (loss.abs() <= e_lse(z, 0.0)).all()
