@@ -389,6 +389,10 @@ int check_dims(int64_t M, int64_t N, int64_t K) {
     return M < 0 || N < 0 || K < 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim ? TGEMM_ERR_INVALID : TGEMM_OK;
 }
 
+// Whether an output of M x N has a workspace that 63 bits count (64 parts of fp32
+// sums; no memory holds an output anywhere near the bound).
+bool countable(int64_t M, int64_t N) { return N == 0 || M <= (int64_t(1) << 54) / N; }
+
 // The plan of a linear layer. What the tile kernel cannot end itself (offsets
 // past 31 bits, fewer than 8 columns) goes through the join.
 int plan_linear(int64_t M, int64_t N, int64_t K, int type, int64_t ldx, int64_t ldw, int w_layout, int y_type,
@@ -399,6 +403,7 @@ int plan_linear(int64_t M, int64_t N, int64_t K, int type, int64_t ldx, int64_t 
     if ((k_step != 0 && k_step != 32 && k_step != 64) || splits < 0 || splits > kMaxSplits) return TGEMM_ERR_INVALID;
     const int64_t wmin = w_layout == TGEMM_B_NxK ? K : N;
     if (ldx < (K > 1 ? K : 1) || ldw < (wmin > 1 ? wmin : 1) || ldy < (N > 1 ? N : 1)) return TGEMM_ERR_INVALID;
+    if (!countable(M, N)) return TGEMM_ERR_UNSUPPORTED;
     const bool direct = N >= 8 && fits31(ldy, N, esize(y_type));
     *ncu = 256;
     if (M > 0 && N > 0 && K > 0) {
@@ -415,6 +420,7 @@ int plan_tn(int64_t M, int64_t N, int64_t K, int type, int64_t lda, int64_t ldb,
     if (check_dims(M, N, K) != TGEMM_OK || !is16(type) || (c_type != type && c_type != TGEMM_F32)) return TGEMM_ERR_INVALID;
     if ((k_step != 0 && k_step != 32 && k_step != 64) || splits < 0 || splits > kMaxSplits) return TGEMM_ERR_INVALID;
     if (lda < (M > 1 ? M : 1) || ldb < (N > 1 ? N : 1) || ldc < (N > 1 ? N : 1)) return TGEMM_ERR_INVALID;
+    if (!countable(M, N)) return TGEMM_ERR_UNSUPPORTED;
     const bool direct = N >= 8 && fits31(ldc, N, esize(c_type));
     *ncu = 256;
     if (M > 0 && N > 0 && K > 0) {
@@ -868,6 +874,7 @@ int plan_linear_grad(int64_t M, int64_t N, int64_t K, int type, bool f32, int64_
     if (w_layout != TGEMM_B_KxN && w_layout != TGEMM_B_NxK) return TGEMM_ERR_INVALID;
     if (act < TGEMM_ACT_NONE || act > TGEMM_ACT_GELU_TANH) return TGEMM_ERR_INVALID;
     if (lddy < (N > 1 ? N : 1)) return TGEMM_ERR_INVALID;
+    if (!countable(M, N) || !countable(M, K) || !countable(N, K)) return TGEMM_ERR_UNSUPPORTED;
     const bool nxk = w_layout == TGEMM_B_NxK, own = f32 || act != TGEMM_ACT_NONE;
     x->ldp = own ? up(N > 0 ? N : 1, 64) : lddy;
     x->off_scale = own ? up(M * x->ldp * 2, 256) : 0;

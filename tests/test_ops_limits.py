@@ -1,5 +1,5 @@
 """Refusals of the operators' entry points on the host, beside
-test_ops_boundary.py: gradients of an fp32 result."""
+test_ops_boundary.py: gradients of an fp32 result, sizes past 64 bits."""
 import pytest
 
 import dense_tiled_gemm_tgemm_amd as tg
@@ -48,3 +48,16 @@ def linear_grad(**kw):
     dict(dY=None), dict(dY=P[3] + 2), dict(dX=P[0]), dict(dW=P[1]), dict(dX=P[5]), dict(dbias=P[4]), dict(dW=P[3] + 2)])
 def test_linear_grad_f32_refuses(kw):
     assert linear_grad(**kw) == INV
+
+
+def test_workspaces_past_63_bits_are_refused():
+    """Sizes that the header allows and no memory holds: refused, not wrapped."""
+    big, UNS = 2 ** 31 - 1, tg.TGEMM_ERR_UNSUPPORTED
+    assert tg.tgemm_linear_workspace(big, big, 4, "bf16", 4, 4, "NxK", "bf16", big) == UNS
+    assert tg.tgemm_tn_workspace(big, big, 4, "bf16", big, big, "bf16", big) == UNS
+    for query in (tg.tgemm_linear_grad_workspace, tg.tgemm_linear_grad_f32_workspace):
+        for act in ("none", "silu"):
+            assert query(big, big, 4, "bf16", 4, 4, "NxK", act, big, 4, 4) == UNS
+            assert query(big, 4, big, "bf16", big, big, "NxK", act, 4, big, big) == UNS
+            assert query(4, big, big, "bf16", big, big, "NxK", act, big, big, big) == UNS
+    assert tg.tgemm_linear_workspace(big, 0, 4, "bf16", 4, 4, "NxK", "bf16", 1) == 0
