@@ -400,3 +400,176 @@ def test_xent_of_more_rows_than_one_grid():
     # (the exponential against the maximum is one step of log2(e) z away from 1)
     z = h[:, 3].float()
     assert ((lse - z).abs() <= e_lse(z, 0.0)).all() and (loss.abs() <= e_lse(z, 0.0)).all()
+
+
+# ------------------------------------- walks over several tiles, and pieces --
+
+@pytest.mark.parametrize("K", [130, 515, 128])
+@pytest.mark.parametrize("layout", ["NxK", "KxN"])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_linear_walk(dtype, layout, K):
+    """More 256-row tiles than compute units (17 x 18), ragged in every axis: the
+    load stream goes on from one tile to the next around each end of tile. With
+    residual and pre-activation; bit for bit with tiles of 128 rows, and sampled
+    rows and columns against 64 bits."""
+    M, N = 4200, 4401
+    g = torch.Generator(device="cuda").manual_seed(K)
+    x = torch.randn((M, K), generator=g, device="cuda").to(dtype)
+    w = (torch.randn((N, K), generator=g, device="cuda") * K ** -0.5).to(dtype)
+    b, r = torch.randn((N,), generator=g, device="cuda"), torch.randn((M, N), generator=g, device="cuda").to(dtype)
+    wl = w if layout == "NxK" else w.t().contiguous()
+    for out in (dtype, F32):
+        y = tg.linear(x, wl, b, "silu", r, out_dtype=out, w_layout=layout, tile_m=256, k_step=64, splits=1)
+        z = tg.linear(x, wl, b, "silu", r, out_dtype=out, w_layout=layout, tile_m=128, k_step=64, splits=1)
+        assert torch.equal(y, z)
+        plain = tg.linear(x, wl, b, "silu", None, out_dtype=out, w_layout=layout, tile_m=256, k_step=64, splits=1)
+        for rows, cols in ((slice(None, None, 149), slice(None)), (slice(None), slice(None, None, 157)), (slice(-3, None), slice(None))):
+            xs, ws, bs, rs = x[rows].cpu(), w[cols].cpu(), b[cols].cpu(), r[rows, cols].cpu()
+            p, ref, e = forward64(xs, ws, bs, "silu", rs)
+            within(y[rows, cols], ref, y_tol(p, ref, e, out, rs), "y")
+            p, ref, e = forward64(xs, ws, bs, "silu", None)
+            within(plain[rows, cols], ref, y_tol(p, ref, e, out, None), "plain")
+    # through autograd: pre is kept; automatic choices
+    xd, wd, bd, rd = (q.clone().requires_grad_() for q in (x, wl, b, r))
+    y = tg.linear(xd, wd, bd, "silu", rd, w_layout=layout)
+    dy = torch.randn((M, N), generator=g, device="cuda").to(dtype)
+    gx, gw, gb = torch.autograd.grad(y, [xd, wd, bd], dy)
+    p = x.double() @ w.double().t() + b.double()
+    e = (K + 6) * U * (x.double().abs() @ w.double().abs().t()) + 2 * U * p.abs()
+    h, d64 = half_step(dtype), dy.double()
+    dp = d64 * act_grad64(p, "silu")
+    ep = d64.abs() * (1.2 * (e + h * 1.01 * p.abs() + tiny(dtype)) + 2.0 ** -20)
+    er = ep + h * 1.01 * dp.abs() + tiny(dtype)
+    want = dp @ w.double()
+    within(gx, want.cpu(), (1.01 * (er @ w.double().abs()) + (N + 4) * U * (dp.abs() @ w.double().abs()) + h * 1.02 * want.abs()
+                            + tiny(dtype)).cpu(), "dx")
+    want = dp.t() @ x.double()
+    within(gw if layout == "NxK" else gw.t(), want.cpu(),
+           (1.01 * (er.t() @ x.double().abs()) + (M + 4) * U * (dp.abs().t() @ x.double().abs()) + h * 1.02 * want.abs()
+            + tiny(dtype)).cpu(), "dw")
+    want = dp.sum(0)
+    within(gb, want.cpu(), (ep.sum(0) + (M + 4) * U * dp.abs().sum(0) + 2 * U * want.abs()).cpu(), "db")
+
+
+@pytest.mark.parametrize("K", [130, 515, 128])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_gemm_tn_walk(dtype, K):
+    """The same for A^T B, into fp32 and 16 bits, with what C holds added."""
+    M, N = 4200, 4401
+    g = torch.Generator(device="cuda").manual_seed(K)
+    a = torch.randn((K, M + 3), generator=g, device="cuda").to(dtype)[:, :M]
+    b = torch.randn((K, N + 2), generator=g, device="cuda").to(dtype)[:, :N]
+    ad, bd = a.double(), b.double()
+    ref, s = ad.t() @ bd, ad.abs().t() @ bd.abs()
+    for out in (dtype, F32):
+        c0 = torch.randn((M, N), generator=g, device="cuda").to(out)
+        got = [tg.gemm_tn(a, b, out_dtype=out, tile_m=tm, k_step=64, splits=1) for tm in (256, 128)]
+        acc = [tg.gemm_tn(a, b, out=c0.clone(), accumulate=True, tile_m=tm, k_step=64, splits=1) for tm in (256, 128)]
+        assert torch.equal(*got) and torch.equal(*acc)
+        within(got[0], ref.cpu(), ((K + 4) * U * s + half_step(out) * 1.01 * ref.abs() + tiny(out)).cpu(), "c")
+        want = ref + c0.double()
+        within(acc[0], want.cpu(), ((K + 4) * U * s + 2 * U * (want.abs() + c0.double().abs()) + half_step(out) * 1.01 * want.abs()
+                                    + tiny(out)).cpu(), "c + c0")
+
+
+def check_xent_step(R, V, D, dtype, rows, cols, dlse=False, ignored=0.1, scale=2.0, **kw):
+    """Loss, lse and the gradients of all rows and of the weight's rows `cols` against 64 bits."""
+    g = torch.Generator(device="cuda").manual_seed(R + V + D)
+    h = torch.randn((R, D), generator=g, device="cuda").to(dtype).requires_grad_()
+    w = (torch.randn((V, D), generator=g, device="cuda") * scale * D ** -0.5).to(dtype).requires_grad_()
+    t = torch.randint(0, V, (R,), generator=g, device="cuda")
+    t[torch.rand((R,), generator=g, device="cuda") < ignored] = -100
+    cols = torch.tensor(cols, device="cuda")
+    t[5:5 + len(cols)] = cols                        # targets at the sampled columns
+    t[-1] = V - 1
+    e = torch.randn((R,), generator=g, device="cuda") if dlse else torch.zeros(R, device="cuda")
+    if dlse:
+        loss, lse = tg.linear_cross_entropy(h, w, t, reduction="sum", return_lse=True, **kw)
+        gh, gw = torch.autograd.grad([loss, lse], [h, w], [torch.ones_like(loss), e])
+    else:
+        loss = tg.linear_cross_entropy(h, w, t, reduction="sum", **kw)
+        gh, gw = torch.autograd.grad(loss, [h, w])
+    hd, wd = h.detach().double(), w.detach().double()
+    idx = torch.arange(0, R, max(R // rows, 1), device="cuda")
+    l64 = torch.cat([torch.logsumexp(hd[i:i + 512] @ wd.t(), 1) for i in range(0, R, 512)])
+    valid = t >= 0
+    zt = (hd * wd[t.clamp(min=0)]).sum(1)
+    l = ((l64 - zt) * valid).sum()
+    # (norms bound the sums of absolute values)
+    ez = (D + 4) * U * float(hd.norm(dim=1).max() * wd.norm(dim=1).max())
+    el = ez + 2.0 ** -20 + 4 * U * float(l64.abs().max())
+    within(loss, l.cpu(), ((el + ez) * valid.sum() + 8 * U * l.abs()).cpu(), "loss")
+    if dlse:
+        within(lse, l64.cpu(), torch.full_like(l64, el).cpu(), "lse")
+    hs = half_step(dtype)
+    a, ge = valid.double(), e.double()
+    top = float(torch.maximum((a + ge).abs(), ge.abs()).max().clamp(min=1))
+    once = dtype == BF and not dlse and not kw.get("recompute") and R >= 33
+
+    def coefs(i, c):
+        p = torch.exp(hd[i] @ wd[c].t() - l64[i, None])
+        hot = (t[i, None] == (torch.arange(V, device="cuda") if isinstance(c, slice) else c)[None, :]).double()
+        pa = (a + ge)[i, None].abs() * p
+        G = (a + ge)[i, None] * p - a[i, None] * hot
+        eG = pa * (ez + el + 2.0 ** -20) + 4 * U * (pa + a[i, None] * hot)
+        if once:
+            eG = eG + hs * 1.01 * pa * (1 - hot)
+        eG = eG + hs * 1.01 * (G.abs() + eG) + (2.0 ** -39 * top if dtype == HF else 0.0)
+        return G, eG * ((a != 0) | (ge != 0))[i, None]
+
+    G, eG = coefs(idx, slice(None))
+    want = G @ wd
+    within(gh[idx], want.cpu(), (1.01 * (eG @ wd.abs()) + (V + 4) * U * (G.abs() @ wd.abs()) + hs * 1.02 * want.abs()
+                                 + tiny(dtype)).cpu(), "dh")
+    G, eG = coefs(slice(None), cols)
+    want = G.t() @ hd
+    within(gw[cols], want.cpu(), (1.01 * (eG.t() @ hd.abs()) + (R + 4) * U * (G.abs().t() @ hd.abs()) + hs * 1.02 * want.abs()
+                                  + tiny(dtype)).cpu(), "dw")
+
+
+@pytest.mark.parametrize("dtype,kw", [(BF, {}), (BF, {"recompute": True}), (HF, {}), (BF, {"dlse": True})])
+def test_xent_walk(dtype, kw):
+    """Long rows over many tiles (17 x 79 of 256 rows: walks), ragged in every axis."""
+    check_xent_step(4200, 20001, 1030, dtype, 40, [0, 255, 256, 1023, 12345, 19999, 20000], **kw)
+
+
+def test_xent_streamed_exponentials():
+    """More than 512 MiB of exponentials: stored past the caches."""
+    check_xent_step(4100, 70001, 640, BF, 20, [0, 127, 128, 69887, 69888, 70000])
+
+
+@pytest.mark.parametrize("dtype,kw", [(BF, {"recompute": True}), (HF, {"dlse": True}), (HF, {})])
+def test_xent_seams_of_the_pieces(dtype, kw):
+    """Three pieces of the vocabulary, 23552, 23552 and 22897 columns: the weight's
+    rows and targets on both sides of each seam, running sums over the pieces."""
+    check_xent_step(9000, 70001, 16, dtype, 20,
+                    [0, 1, 23550, 23551, 23552, 23553, 47102, 47103, 47104, 47105, 69999, 70000], scale=0.5, **kw)
+
+
+def test_xent_recompute_keeps_no_logits():
+    """recompute=True: a step's memory is its gradients, 2^28 coefficients (512 MiB)
+    and the sums of split products, and the forward pass alone keeps rows, where
+    fp32 logits take 3.7 GB; with gradients at once it is 2 bytes a logit."""
+    R, V, D = 8192, 114_688, 64
+    h = torch.randn((R, D), device="cuda").to(BF).requires_grad_()
+    w = torch.randn((V, D), device="cuda").to(BF).requires_grad_()
+    t = torch.randint(0, V, (R,), device="cuda")
+
+    def peak(fn):
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        torch.cuda.reset_peak_memory_stats()
+        base = torch.cuda.memory_allocated()
+        fn()
+        return torch.cuda.max_memory_allocated() - base
+
+    loss = []
+    forward = peak(lambda: loss.append(tg.linear_cross_entropy(h, w, t, recompute=True)))
+    # parts of 128 columns (8 bytes), and a handful of fp32 rows
+    assert forward <= R * (V // 128) * 8 + 64 * R + (1 << 20)
+    backward = peak(lambda: torch.autograd.grad(loss[0], [h, w]))
+    sums = 2 ** 28 * 2 * 1.05 + 65 * R * D * 4 + 64 * 4 * 2 ** 28 // R * D
+    assert backward <= sums + 2 * (R + V) * D * 2, (backward, sums)
+    del loss
+    at_once = peak(lambda: torch.autograd.grad(tg.linear_cross_entropy(h, w, t), [h, w]))
+    assert at_once <= R * (V + 128) * 2 + R * (V // 128) * 8 + 64 * 4 * (R + V) * D + 2 * (R + V) * D * 2 + (1 << 20)
