@@ -377,6 +377,7 @@ def gemm_tn(A, B, out=None, out_dtype=None, alpha: float = 1.0, accumulate: bool
     if B.shape[0] != K:
         raise ValueError(f"the long axes differ: A is {tuple(A.shape)}, B is {tuple(B.shape)}")
     _no_tangents(torch, A, B, out)
+    given = out is not None
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
@@ -389,6 +390,8 @@ def gemm_tn(A, B, out=None, out_dtype=None, alpha: float = 1.0, accumulate: bool
     _device(out, "out", A.device)
     if out.dtype not in (A.dtype, torch.float32):
         raise TypeError(f"out must be {A.dtype} or float32, got {out.dtype}")
+    if out.requires_grad and torch.is_grad_enabled():
+        raise ValueError("out requires a gradient; writes have no history")
     ldc = _rows(out)
     if ldc is None:
         raise ValueError("out must have unit column stride and rows that do not overlap")
@@ -404,6 +407,8 @@ def gemm_tn(A, B, out=None, out_dtype=None, alpha: float = 1.0, accumulate: bool
                              alpha, 1 if accumulate else 0, ws_ptr, need, _stream(torch, dev), tile_m, k_step, splits)
     if rc != TGEMM_OK:
         raise TgemmError(rc, f"gemm_tn M={M} N={N} K={K} {A.dtype}->{out.dtype}")
+    if given and not out.is_inference():
+        torch.autograd.graph.increment_version(out)   # what autograd has saved of out is stale
     return out
 
 

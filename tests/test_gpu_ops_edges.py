@@ -573,3 +573,24 @@ def test_xent_recompute_keeps_no_logits():
     del loss
     at_once = peak(lambda: torch.autograd.grad(tg.linear_cross_entropy(h, w, t), [h, w]))
     assert at_once <= R * (V + 128) * 2 + R * (V // 128) * 8 + 64 * 4 * (R + V) * D + 2 * (R + V) * D * 2 + (1 << 20)
+
+
+def test_gemm_tn_into_a_tensor_that_autograd_keeps():
+    """Writing out marks it as changed: a backward pass that had saved its old values says so."""
+    a, b = rand((20, 16), 1, BF).cuda(), rand((20, 24), 2, BF).cuda()
+    c = rand((16, 24), 3, F32).cuda()
+    s = torch.ones((), device="cuda", requires_grad=True)
+    y = (c * s).sum()                                # keeps c for s's gradient
+    before = c._version
+    tg.gemm_tn(a, b, out=c, accumulate=True)
+    assert c._version > before
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    leaf = torch.zeros((16, 24), device="cuda", requires_grad=True)
+    with pytest.raises(ValueError, match="requires a gradient"):
+        tg.gemm_tn(a, b, out=leaf)
+    with torch.no_grad():
+        tg.gemm_tn(a, b, out=leaf)                   # as an optimizer would
+    assert leaf.abs().max() > 0
+    with torch.inference_mode():
+        assert torch.equal(tg.gemm_tn(a, b, out=torch.zeros((16, 24), device="cuda"), accumulate=True), tg.gemm_tn(a, b, out_dtype=F32))
