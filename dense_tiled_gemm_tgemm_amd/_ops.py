@@ -721,14 +721,18 @@ def linear_cross_entropy(hidden, weight, target, ignore_index: int = -100, reduc
     A target outside the vocabulary (and not ``ignore_index``) gives NaN.
     Differentiable in hidden and weight. An ignored row's hidden state has to be
     finite. For a "sum" or "mean" of bfloat16 operands without return_lse, of 33
-    rows and at most 2^30 logits, a call under autograd computes the gradients at
-    once, from 16-bit exponentials that live for the call, and keeps them (of
-    the operands' sizes) for the backward pass, which multiplies them by the
-    loss's gradient (one more rounding where that is no power of two) and does
-    nothing where it is 1. Elsewhere, in a second backward pass, and with
-    ``recompute=True`` (a loss that may see no backward pass), the forward pass
-    keeps the rows' log-sum-exp alone and the backward pass computes the logits
-    again in pieces of the vocabulary.
+    rows or more, a call under autograd computes the gradients at once, from
+    16-bit exponentials that live for the call (2 bytes a logit, as much as
+    16-bit logits take), where rows times the vocabulary rounded up to an odd
+    multiple of 64 is at most 2^30. It keeps the gradients (of the operands'
+    sizes) for the backward pass, which multiplies them by the loss's gradient
+    (one more rounding where that is no power of two) and does nothing where it
+    is 1; they are no saved tensors, so hooks on those do not see them, and a
+    checkpointed call computes them twice. Elsewhere, in a second backward pass,
+    and with ``recompute=True`` (a loss that may see no backward pass, a
+    checkpoint, memory that has no room for the logits), the forward pass keeps
+    the rows' log-sum-exp alone and the backward pass computes the logits again
+    in pieces of the vocabulary of at most 2^28 of them.
     """
     import torch
     if reduction not in _REDUCE:

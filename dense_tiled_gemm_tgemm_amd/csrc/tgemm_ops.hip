@@ -111,8 +111,9 @@ void fit_splits(int64_t K, int want, int k_step, int* splits, int* kper) {
 // there two workgroups of 32-deep steps, which cover each other's fixed parts,
 // stay ahead. Rows that start between 16-byte boundaries touch one line more
 // (`late`). Fitted to 3300 timings of 124 random products and weight gradients
-// (33 <= M <= 8192, N to 110000, K to 60000, 15 splits, graph launches): the
-// choice takes 1.0% longer than the fastest on average, 32% at worst.
+// (33 <= M <= 8192, N to 110000, K to 60000, 15 splits, graph launches): over
+// that same set the choice takes 1.0% longer than the fastest on average, 32% at
+// worst.
 double tile_time(int64_t M, int64_t N, int64_t kper, int tile_m, int k_step, int layout, int splits, int ncu, bool join,
                  bool odd) {
     static const double cost[5][3] = {{0.572, 0.675, 0.645}, {0.364, 0.431, 0.416}, {0.277, 0.274, 0.244},

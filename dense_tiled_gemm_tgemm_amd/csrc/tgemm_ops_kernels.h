@@ -610,8 +610,8 @@ __device__ __forceinline__ void end_tile(const f32x4 (&acc)[NI][8], const OpArgs
 // additions (StepCursor; 8192 x 4096 x 8192 in bfloat16: 389 -> 372 us for a B
 // stored K x N, 397 -> 377 for A^T B, whose steps spent 80 of 330 instructions
 // on 64-bit products and comparisons). 256-row tiles are bound by the matrix
-// cores at the clock the card's power leaves them (8192^3: 1560 TFLOP/s, the
-// library product 1600), 128- and 64-row ones by LDS traffic, 40 KiB a step
+// cores at the clock the card's power leaves them (8192^3: 1623 TFLOP/s, the
+// library product 1632), 128- and 64-row ones by LDS traffic, 40 KiB a step
 // and compute unit at 64 rows. kEndAcc32 with splits > 1
 // (grid W * splits): a workgroup computes one part of the K axis of one tile,
 // into that part of C (splits arrays of M x ldc, one after another).

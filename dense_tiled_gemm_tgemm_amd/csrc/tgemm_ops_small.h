@@ -20,9 +20,10 @@ namespace tg {
 // that way, each 16 lanes touch 16 rows and the vector L1 serves 16 bytes a
 // clock; four neighbouring lanes on 64 bytes of one row (row l / 4, chunk l mod
 // 4) are served four times as fast, and ds_bpermute brings the chunks to their
-// lanes. 8 x 12288 x 12288: 69.9 -> 59.7 us (5.1 TB/s of weight), 16 x 4096 x
-// 12288: 30.9 -> 25.1. A's rows come through the caches the same way, or, up to
-// 4 rows (XP = 0), in the operand's layout at once.
+// lanes. 8 x 12288 x 12288: 69.9 -> 58.8 us, 16 x 4096 x 12288: 26.9 -> 21.9
+// (with the steps after it 53.6, 5.6 TB/s of weight, and 21.4). A's rows come
+// through the caches the same way, or, up to 4 rows (XP = 0), in the operand's
+// layout at once.
 __device__ __forceinline__ u32x4 load16_lanes(const BufRsrc& rs, unsigned off, int soff) {
 #if defined(__HIP_DEVICE_COMPILE__)
     return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, (int)off, soff, 0));

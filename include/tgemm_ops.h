@@ -197,10 +197,12 @@ int tgemm_xent_grad(int64_t rows, int64_t vocab, int64_t dim, int type, const vo
  * tgemm_xent and its gradients for a loss gradient of 1 in one call, without
  * computing the logits a second time: dH and dW (each may be NULL) as
  * tgemm_xent_grad gives them for total (dloss 1, `count` for the mean). The
- * exponentials of the logits, 16 bits, live in the workspace (rows * vocab * 2
- * bytes, vocab rounded up to an odd multiple of 64) and become the coefficients there.
- * bfloat16 only, reduction SUM or MEAN, at most 2^30 exponentials:
- * TGEMM_ERR_UNSUPPORTED otherwise. rows >= 1.
+ * exponentials of the logits, 16 bits, live in the workspace (2 bytes each for
+ * rows times vocab rounded up to an odd multiple of 64: as much as 16-bit logits
+ * take) and become the coefficients there: each is rounded twice to 16 bits, but
+ * for the target's.
+ * bfloat16 only, reduction SUM or MEAN, at most 2^30 of them (rows times the
+ * rounded vocab) and 4,000,000 a row: TGEMM_ERR_UNSUPPORTED otherwise. rows >= 1.
  */
 int64_t tgemm_xent_both_workspace(int64_t rows, int64_t vocab, int64_t dim, int type, int64_t ldh, int64_t ldw,
                                   int64_t lddh, int64_t lddw);
