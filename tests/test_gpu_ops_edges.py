@@ -594,3 +594,39 @@ def test_gemm_tn_into_a_tensor_that_autograd_keeps():
     assert leaf.abs().max() > 0
     with torch.inference_mode():
         assert torch.equal(tg.gemm_tn(a, b, out=torch.zeros((16, 24), device="cuda"), accumulate=True), tg.gemm_tn(a, b, out_dtype=F32))
+
+
+def test_captured_step_with_an_f32_result_replays():
+    """A binary16 layer with an fp32 result, its gradients (whose scale is found on
+    the device) and a few rows' loss in a graph: every replay equals the eager
+    results, for gradients of any size, with eager work in between."""
+    x, w = rand((96, 256), 1, HF).cuda(), rand((200, 256), 2, HF, 0.06).cuda()
+    v, t = rand((1000, 200), 3, HF, 0.1).cuda(), torch.randint(0, 1000, (16,)).cuda()
+    dy = rand((96, 200), 4, F32).cuda()
+
+    def step():
+        xs, ws = x.detach().requires_grad_(), w.detach().requires_grad_()
+        b = torch.zeros((200,), device="cuda", requires_grad=True)
+        y = tg.linear(xs, ws, b, "gelu", out_dtype=F32)
+        loss = tg.linear_cross_entropy(y[:16].half(), v, t)
+        return (y.detach(), loss.detach()) + torch.autograd.grad([y, loss], [xs, ws, b], [dy, torch.ones_like(loss)])
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = step()
+    for i, size in enumerate((1.0, 1e-9, 1e7, 1.0)):
+        x.copy_(rand((96, 256), 10 + i, HF))
+        dy.copy_(rand((96, 200), 20 + i, F32) * size)
+        g.replay()
+        torch.cuda.synchronize()
+        want = step()
+        again = step()
+        torch.cuda.synchronize()
+        for a, b, c in zip(out, want, again):
+            assert torch.equal(a, b) and torch.equal(b, c)
+            assert b.abs().max() > 0
